@@ -409,6 +409,105 @@ WKV7_API wkv7_status wkv7_decode_step_raw(int B, int H, int N, wkv7_dtype dt,
                                           const float *r_k, float gn_eps, void *stream);
 
 /*
+ * The gated delta rule, the sister recurrence of WKV-7 with one scalar decay per token and head
+ * (no counterpart on the pages; heads of this kind stand beside WKV-7 heads in hybrid stacks). Per
+ * sequence and value head it carries an N x N fp32 state S (row = value channel, column = key
+ * channel); with the key head hk = h / (H / Hk):
+ *
+ *     q~ = scale q_t[hk],  k~ = k_t[hk]           (qk_norm: q and k first brought to unit length,
+ *                                                  x / sqrt(sum x^2 + norm_eps), per token and head)
+ *     e_t = v_t - exp(g_t) S_{t-1} k~
+ *     S_t = exp(g_t) S_{t-1} + beta_t e_t k~^T
+ *     y_t = S_t q~
+ *
+ * Layouts: q, k [rows][Hk][N]; v, y [rows][H][N]; g, beta [rows][H]; all of dt (y too: it feeds the
+ * next projection in the caller's type, rounded once from fp32). A row is a token: rows = B * T for B
+ * sequences of T tokens, or, with cu_seqlens, T packed rows of B sequences, sequence s holding the
+ * rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1. States [B][H][N][N] fp32. H must be a multiple of Hk;
+ * N is 64 or 128. g is a log decay: any value <= 0, -inf included (the state is reset); positive
+ * values grow the state. beta is any finite value.
+ * q, k and v may be strided by token (heads and channels dense): row strides in elements, multiples
+ * of 16 bytes, at least Hk * N (v: H * N).
+ */
+typedef struct wkv7_delta_opts {
+    float scale;            /* factor of q; 0 = 1 / sqrt(N)                                      */
+    int qk_norm;            /* 1 = q and k are brought to unit length on load; 0 = taken as given */
+    float norm_eps;         /* inside the root of qk_norm's length (default 1e-6, must be > 0)    */
+    const int *cu_seqlens;  /* device int32 [B + 1], non-decreasing from 0, at most T; NULL = B   */
+                            /* sequences of T tokens. Rows from cu_seqlens[B] on are not touched. */
+                            /* Entries outside 0..T or decreasing are clamped: such sequences     */
+                            /* come out wrong, but nothing outside the buffers is accessed.       */
+    long long q_stride, k_stride, v_stride;   /* elements from one row to the next; 0 = dense     */
+} wkv7_delta_opts;
+
+/* Fills *opts with the defaults: scale 1 / sqrt(N), no normalisation, norm_eps 1e-6, equal lengths,
+ * dense rows. */
+WKV7_API void wkv7_delta_opts_default(wkv7_delta_opts *opts);
+
+/*
+ * The gated delta rule over whole sequences. S0 [B][H][N][N] fp32 or NULL (zeros); S_T the same or
+ * NULL (not returned), may equal S0 (in place) and must not otherwise overlap the inputs; a sequence
+ * without tokens hands S0 (or zeros) on. opts NULL = defaults. No workspace.
+ * Errors: WKV7_ERR_ARG (sizes, H not a multiple of Hk, options, NULL / host / too-small buffers,
+ * overlaps), WKV7_ERR_ALIGN (every pointer 16-byte aligned), WKV7_ERR_UNSUPPORTED (N),
+ * WKV7_ERR_CUDA.
+ */
+WKV7_API wkv7_status wkv7_delta_forward(int B, int T, int H, int Hk, int N, wkv7_dtype dt,
+                                        const void *q, const void *k, const void *v, const void *g,
+                                        const void *beta, const float *S0, void *y, float *S_T,
+                                        const wkv7_delta_opts *opts, void *stream);
+
+/*
+ * One token for each of B rows against a pool of n_slots states: row b advances S[slots[b]] in
+ * place. q, k [B][Hk][N], v, y [B][H][N], g, beta [B][H] of dt; S [n_slots][H][N][N] fp32; slots
+ * device int32 [B], or NULL (row b takes slot b; n_slots must then be at least B). A row whose slot
+ * is outside 0..n_slots-1 (-1 for padding) gets y = 0 and touches no state. Rows that name the same
+ * slot are taken one after the other in the order of b. opts as wkv7_delta_forward (cu_seqlens must
+ * be NULL). Errors as wkv7_delta_forward.
+ */
+WKV7_API wkv7_status wkv7_delta_step(int B, int H, int Hk, int N, wkv7_dtype dt, const void *q,
+                                     const void *k, const void *v, const void *g, const void *beta,
+                                     float *S, int n_slots, const int *slots, void *y,
+                                     const wkv7_delta_opts *opts, void *stream);
+
+/*
+ * One step of beam search's selection: of the K beams of each of B requests and the V tokens of the
+ * vocabulary, the M best continuations by
+ *     score(b, j, t) = scores[b][j] + logits[b][j][t] - log(sum_t' exp(logits[b][j][t']))
+ * from the best down; equal scores go to the lowest j * V + t. A beam marked in `finished` offers
+ * only the token eos, at its own score (nothing is read of its logits). A score of -inf or NaN
+ * (masked tokens, dead beams) is never chosen; a NaN logit counts as -inf, and a row with +inf has
+ * no normalised scores and offers nothing. Where fewer than M continuations exist the
+ * rest of the outputs hold score -inf, parent -1 and token -1.
+ * logits   [B][K] rows of V elements of dt, row_stride elements apart (0 = V); any alignment of
+ *          the elements (the base pointer 16-byte aligned as everywhere).
+ * scores   [B][K] fp32.      finished [B][K] bytes (0 or 1) or NULL; eos in 0..V-1 when given.
+ * Outputs  out_scores [B][M] fp32, parents [B][M] int32 (the beam j), tokens [B][M] int32.
+ * Sizes: B, V >= 1, 1 <= K <= 64, 1 <= M <= 64. The normaliser is summed in fp32 per thread and
+ * in fp64 across threads, and scores are compared in fp64 before they are rounded to fp32.
+ * Workspace: wkv7_beam_select_workspace_bytes(B, K, V, M) bytes.
+ * Errors as wkv7_delta_forward, plus WKV7_ERR_WORKSPACE; WKV7_ERR_UNSUPPORTED for K or M above 64.
+ */
+#define WKV7_BEAM_MAX 64
+WKV7_API size_t wkv7_beam_select_workspace_bytes(int B, int K, int V, int M);
+WKV7_API wkv7_status wkv7_beam_select(int B, int K, int V, int M, wkv7_dtype dt, const void *logits,
+                                      long long row_stride, const float *scores,
+                                      const unsigned char *finished, int eos, float *out_scores,
+                                      int *parents, int *tokens, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+/*
+ * Moves the rows of recurrent states (or anything else kept per beam) to the beams that
+ * wkv7_beam_select picked: dst[l][b][j] = src[l][b][parents[b][j]] for l < L, b < B, j < K, each row
+ * row_bytes bytes (a multiple of 16). dst may be src (in place: rows that stay are neither read for
+ * themselves nor written); otherwise the two must not overlap. parents device int32 [B][K]; a value
+ * outside 0..K-1 (as -1) keeps row j. 1 <= K <= 64; L, B >= 1. No workspace.
+ * Errors as wkv7_delta_forward.
+ */
+WKV7_API wkv7_status wkv7_beam_reorder(int L, int B, int K, size_t row_bytes, const int *parents,
+                                       const void *src, void *dst, void *stream);
+
+/*
  * Synchronises `stream`, then reports whether a kernel of this library gave up one
  * of its bounded device-side waits since the last call (WKV7_ERR_TIMEOUT; the
  * affected outputs are then incomplete) and clears the flag. Kernels never trap or

@@ -18,7 +18,9 @@
 
 #include "common.cuh"
 #include "backward.cuh"
+#include "beam.cuh"
 #include "decode.cuh"
+#include "delta.cuh"
 #include "epilogue.cuh"
 
 namespace wkv7 {
@@ -803,6 +805,192 @@ wkv7_status wkv7_epilogue_backward(int B, int T, int H, int N, wkv7_dtype dt, co
     a.stream = static_cast<cudaStream_t>(stream);
     const cudaError_t e = wkv7::launch_epilogue_backward(a);
     return e == cudaSuccess ? WKV7_OK : cuda_fail(e, "epilogue backward launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+// Sizes and options shared by the gated delta rule's entries; fills `opts` (defaults if NULL) and the
+// number of rows.
+wkv7_status delta_args(int B, int T, int H, int Hk, int N, wkv7_dtype dt, const wkv7_delta_opts *opts_in,
+                       wkv7_delta_opts &opts, size_t &rows) {
+    if (B <= 0 || T < 0 || H <= 0 || Hk <= 0 || N <= 0)
+        return fail(WKV7_ERR_ARG, "bad sizes B=%d T=%d H=%d Hk=%d N=%d (need B, H, Hk, N >= 1, T >= 0)", B, T, H, Hk, N);
+    if (H % Hk) return fail(WKV7_ERR_ARG, "H=%d is not a multiple of Hk=%d", H, Hk);
+    if (N != 64 && N != 128) return fail(WKV7_ERR_UNSUPPORTED, "head size N=%d: N=64 and N=128 are implemented", N);
+    if (dt != WKV7_F32 && dt != WKV7_BF16) return fail(WKV7_ERR_ARG, "unknown dtype %d", (int)dt);
+    if (static_cast<long long>(B) * H > INT_MAX / 16)
+        return fail(WKV7_ERR_ARG, "B*H=%lld heads: at most %d", static_cast<long long>(B) * H, INT_MAX / 16);
+    wkv7_delta_opts_default(&opts);
+    if (opts_in) opts = *opts_in;
+    if (!std::isfinite(opts.scale)) return fail(WKV7_ERR_ARG, "scale must be finite");
+    if (opts.qk_norm != 0 && opts.qk_norm != 1) return fail(WKV7_ERR_ARG, "qk_norm=%d: must be 0 or 1", opts.qk_norm);
+    if (!(opts.norm_eps > 0.f) || !std::isfinite(opts.norm_eps)) return fail(WKV7_ERR_ARG, "norm_eps must be finite and > 0");
+    if (opts.scale == 0.f) opts.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(N)));
+    const long long dense[] = {(long long)Hk * N, (long long)Hk * N, (long long)H * N};
+    long long *const strides[] = {&opts.q_stride, &opts.k_stride, &opts.v_stride};
+    const char *names[] = {"q_stride", "k_stride", "v_stride"};
+    for (int i = 0; i < 3; ++i) {
+        if (*strides[i] == 0) *strides[i] = dense[i];
+        if (*strides[i] < dense[i] || (*strides[i] * elem_bytes(dt)) % 16 || *strides[i] > (1ll << 40))
+            return fail(WKV7_ERR_ARG, "%s=%lld: at least %lld and a multiple of 16 bytes", names[i], *strides[i], dense[i]);
+    }
+    rows = 1;
+    size_t tok = 1;
+    if (!mul_ok(rows, opts.cu_seqlens ? 1 : B) || !mul_ok(rows, T)) return fail(WKV7_ERR_ARG, "sizes overflow");
+    tok = rows;
+    if (!mul_ok(tok, H) || !mul_ok(tok, N) || tok > (size_t(1) << 40) || rows > (size_t(1) << 40))
+        return fail(WKV7_ERR_ARG, "sizes overflow");
+    return WKV7_OK;
+}
+
+// Bytes that `rows` rows of `width` elements reach over, `stride` elements apart.
+size_t strided_bytes(size_t rows, size_t width, long long stride, wkv7_dtype dt) {
+    return rows ? ((rows - 1) * static_cast<size_t>(stride) + width) * elem_bytes(dt) : 0;
+}
+
+wkv7::DeltaArgs delta_launch(int B, int T, int H, int Hk, int N, wkv7_dtype dt, const void *q, const void *k,
+                             const void *v, const void *g, const void *beta, void *y, const wkv7_delta_opts &o,
+                             void *stream) {
+    wkv7::DeltaArgs p{};
+    p.B = B; p.T = T; p.H = H; p.Hk = Hk; p.N = N; p.dt = dt;
+    p.q = q; p.k = k; p.v = v; p.g = g; p.beta = beta; p.y = y;
+    p.cu = o.cu_seqlens;
+    p.qs = o.q_stride; p.ks = o.k_stride; p.vs = o.v_stride;
+    p.scale = o.scale; p.qk_norm = o.qk_norm; p.norm_eps = o.norm_eps;
+    p.stream = static_cast<cudaStream_t>(stream);
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+void wkv7_delta_opts_default(wkv7_delta_opts *o) {
+    if (!o) return;
+    std::memset(o, 0, sizeof(*o));
+    o->norm_eps = 1e-6f;
+}
+
+wkv7_status wkv7_delta_forward(int B, int T, int H, int Hk, int N, wkv7_dtype dt, const void *q, const void *k,
+                               const void *v, const void *g, const void *beta, const float *S0, void *y, float *S_T,
+                               const wkv7_delta_opts *opts_in, void *stream) {
+    g_err[0] = '\0';
+    wkv7_delta_opts o;
+    size_t rows = 0;
+    wkv7_status st = delta_args(B, T, H, Hk, N, dt, opts_in, o, rows);
+    if (st != WKV7_OK) return st;
+    const size_t kw = size_t(Hk) * N, vw = size_t(H) * N, gb = rows * H * elem_bytes(dt);
+    const size_t sb = size_t(B) * H * N * N * 4;
+    const Buf bufs[] = {{"q", q, strided_bytes(rows, kw, o.q_stride, dt)},
+                        {"k", k, strided_bytes(rows, kw, o.k_stride, dt)},
+                        {"v", v, strided_bytes(rows, vw, o.v_stride, dt)},
+                        {"g", g, gb},
+                        {"beta", beta, gb},
+                        {"cu_seqlens", o.cu_seqlens, o.cu_seqlens ? size_t(B + 1) * 4 : 0},
+                        {"S0", S0, S0 ? sb : 0},
+                        {"y", y, rows * vw * elem_bytes(dt)},
+                        {"S_T", S_T, S_T ? sb : 0}};
+    st = check_buffers(bufs, 9, 7, [&](int x, int i) { return (x == 8 && i == 6 && S_T == S0); });
+    if (st != WKV7_OK) return st;
+    wkv7::DeltaArgs p = delta_launch(B, T, H, Hk, N, dt, q, k, v, g, beta, y, o, stream);
+    p.S0 = S0;
+    p.S_T = S_T;
+    const cudaError_t e = wkv7::launch_delta_forward(p);
+    return e == cudaSuccess ? WKV7_OK : cuda_fail(e, "gated-delta forward launch");
+}
+
+wkv7_status wkv7_delta_step(int B, int H, int Hk, int N, wkv7_dtype dt, const void *q, const void *k, const void *v,
+                            const void *g, const void *beta, float *S, int n_slots, const int *slots, void *y,
+                            const wkv7_delta_opts *opts_in, void *stream) {
+    g_err[0] = '\0';
+    wkv7_delta_opts o;
+    size_t rows = 0;
+    wkv7_status st = delta_args(B, 1, H, Hk, N, dt, opts_in, o, rows);
+    if (st != WKV7_OK) return st;
+    if (o.cu_seqlens) return fail(WKV7_ERR_ARG, "cu_seqlens must be NULL: a step takes one token per row");
+    if (n_slots <= 0) return fail(WKV7_ERR_ARG, "n_slots=%d: at least 1", n_slots);
+    if (!slots && n_slots < B) return fail(WKV7_ERR_ARG, "n_slots=%d < B=%d without slots", n_slots, B);
+    size_t sb = 4;
+    if (!mul_ok(sb, n_slots) || !mul_ok(sb, H) || !mul_ok(sb, N) || !mul_ok(sb, N) || sb > (size_t(1) << 42))
+        return fail(WKV7_ERR_ARG, "sizes overflow");
+    const size_t kw = size_t(Hk) * N, vw = size_t(H) * N, gb = rows * H * elem_bytes(dt);
+    const Buf bufs[] = {{"q", q, strided_bytes(rows, kw, o.q_stride, dt)},
+                        {"k", k, strided_bytes(rows, kw, o.k_stride, dt)},
+                        {"v", v, strided_bytes(rows, vw, o.v_stride, dt)},
+                        {"g", g, gb},
+                        {"beta", beta, gb},
+                        {"slots", slots, slots ? size_t(B) * 4 : 0},
+                        {"S", S, sb},
+                        {"y", y, rows * vw * elem_bytes(dt)}};
+    st = check_buffers(bufs, 8, 6, [](int, int) { return false; });
+    if (st != WKV7_OK) return st;
+    wkv7::DeltaArgs p = delta_launch(B, 1, H, Hk, N, dt, q, k, v, g, beta, y, o, stream);
+    p.S = S;
+    p.n_slots = n_slots;
+    p.slots = slots;
+    const cudaError_t e = wkv7::launch_delta_step(p);
+    return e == cudaSuccess ? WKV7_OK : cuda_fail(e, "gated-delta step launch");
+}
+
+static bool beam_sizes_ok(int B, int K, int V, int M) {
+    if (B <= 0 || K <= 0 || V <= 0 || M <= 0 || K > WKV7_BEAM_MAX || M > WKV7_BEAM_MAX || V > INT_MAX - 65536)
+        return false;
+    // segments of at least 2048 elements index the grid
+    return static_cast<long long>(B) * K * (V / 2048 + 2) <= INT_MAX;
+}
+
+size_t wkv7_beam_select_workspace_bytes(int B, int K, int V, int M) {
+    return beam_sizes_ok(B, K, V, M) ? wkv7::beam_select_workspace(B, K, V, M) : 0;
+}
+
+wkv7_status wkv7_beam_select(int B, int K, int V, int M, wkv7_dtype dt, const void *logits, long long row_stride,
+                             const float *scores, const unsigned char *finished, int eos, float *out_scores,
+                             int *parents, int *tokens, void *workspace, size_t workspace_bytes, void *stream) {
+    g_err[0] = '\0';
+    if (B <= 0 || K <= 0 || V <= 0 || M <= 0)
+        return fail(WKV7_ERR_ARG, "bad sizes B=%d K=%d V=%d M=%d (need all >= 1)", B, K, V, M);
+    if (K > WKV7_BEAM_MAX || M > WKV7_BEAM_MAX)
+        return fail(WKV7_ERR_UNSUPPORTED, "K=%d beams, M=%d picks: at most %d", K, M, WKV7_BEAM_MAX);
+    if (!beam_sizes_ok(B, K, V, M)) return fail(WKV7_ERR_ARG, "sizes overflow");
+    if (dt != WKV7_F32 && dt != WKV7_BF16) return fail(WKV7_ERR_ARG, "unknown dtype %d", (int)dt);
+    if (row_stride == 0) row_stride = V;
+    if (row_stride < V || row_stride > (1ll << 40)) return fail(WKV7_ERR_ARG, "row_stride=%lld: at least V=%d", row_stride, V);
+    if (finished && (eos < 0 || eos >= V)) return fail(WKV7_ERR_ARG, "eos=%d outside 0..%d", eos, V - 1);
+    const size_t need = wkv7::beam_select_workspace(B, K, V, M), rows = size_t(B) * K, outs = size_t(B) * M * 4;
+    if (!workspace || workspace_bytes < need)
+        return fail(WKV7_ERR_WORKSPACE, "workspace of %zu bytes required, %zu given", need, workspace ? workspace_bytes : 0);
+    const Buf bufs[] = {{"logits", logits, strided_bytes(rows, V, row_stride, dt)},
+                        {"scores", scores, rows * 4},
+                        {"finished", finished, finished ? rows : 0},
+                        {"out_scores", out_scores, outs},
+                        {"parents", parents, outs},
+                        {"tokens", tokens, outs},
+                        {"workspace", workspace, need}};
+    const wkv7_status st = check_buffers(bufs, 7, 3, [](int, int) { return false; });
+    if (st != WKV7_OK) return st;
+    const wkv7::BeamArgs p{B, K, V, M, dt, logits, row_stride, scores, finished, eos, out_scores, parents, tokens,
+                           workspace, static_cast<cudaStream_t>(stream)};
+    const cudaError_t e = wkv7::launch_beam_select(p);
+    return e == cudaSuccess ? WKV7_OK : cuda_fail(e, "beam selection launch");
+}
+
+wkv7_status wkv7_beam_reorder(int L, int B, int K, size_t row_bytes, const int *parents, const void *src, void *dst,
+                              void *stream) {
+    g_err[0] = '\0';
+    if (L <= 0 || B <= 0 || K <= 0) return fail(WKV7_ERR_ARG, "bad sizes L=%d B=%d K=%d (need all >= 1)", L, B, K);
+    if (K > WKV7_BEAM_MAX) return fail(WKV7_ERR_UNSUPPORTED, "K=%d beams: at most %d", K, WKV7_BEAM_MAX);
+    if (row_bytes == 0 || row_bytes % 16) return fail(WKV7_ERR_ARG, "row_bytes=%zu: a multiple of 16", row_bytes);
+    size_t bytes = row_bytes, blocks = row_bytes / (8 * 256) + 1;
+    if (!mul_ok(bytes, L) || !mul_ok(bytes, B) || !mul_ok(bytes, K) || !mul_ok(blocks, L) || !mul_ok(blocks, B) ||
+        bytes > (size_t(1) << 42) || blocks > size_t(INT_MAX))
+        return fail(WKV7_ERR_ARG, "sizes overflow");
+    const Buf bufs[] = {{"parents", parents, size_t(B) * K * 4}, {"src", src, bytes}, {"dst", dst, bytes}};
+    const wkv7_status st = check_buffers(bufs, 3, 2, [&](int x, int i) { return x == 2 && i == 1 && src == dst; });
+    if (st != WKV7_OK) return st;
+    const cudaError_t e = wkv7::launch_beam_reorder(L, B, K, row_bytes, parents, src, dst, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? WKV7_OK : cuda_fail(e, "beam reorder launch");
 }
 
 }  // extern "C"

@@ -1,0 +1,52 @@
+// Arguments of the gated delta rule's kernels after validation, and what they share.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "wkv7.h"
+
+namespace wkv7 {
+
+struct DeltaArgs {
+    int B, T;               // sequences; tokens per sequence, or rows in all when packed
+    int H, Hk, N;
+    wkv7_dtype dt;
+    const void *q, *k, *v, *g, *beta;
+    const float *S0;        // nullable: zero initial state
+    void *y;
+    float *S_T;             // nullable
+    const int *cu;          // nullable: B sequences of T tokens
+    long long qs, ks, vs;   // row strides of q, k, v in elements
+    float scale;
+    int qk_norm;
+    float norm_eps;
+    // step: the pool
+    float *S;
+    int n_slots;
+    const int *slots;       // nullable: row b takes slot b
+    cudaStream_t stream;
+};
+
+cudaError_t launch_delta_forward(const DeltaArgs &p);
+cudaError_t launch_delta_step(const DeltaArgs &p);
+
+// Rows [first, last) of sequence s. Packed bounds outside 0..T or decreasing are clamped, so that no
+// row outside the buffers is reached.
+__device__ __forceinline__ void delta_rows(const int *cu, int T, int s, long long &first, long long &last) {
+    if (!cu) {
+        first = (long long)s * T;
+        last = first + T;
+        return;
+    }
+    const int a = min(max(cu[s], 0), T), b = min(max(cu[s + 1], a), T);
+    first = a;
+    last = b;
+}
+
+// exp(g) of a log decay. Values below -120 (exp is 0 in fp32, denormals included), -inf among them,
+// count as -120, so that differences of sums of decays stay finite; a NaN stays one.
+__device__ __forceinline__ float delta_clamp(float g) { return g < -120.f ? -120.f : g; }
+
+}  // namespace wkv7

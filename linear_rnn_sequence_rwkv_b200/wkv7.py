@@ -11,7 +11,9 @@ outputs are copied back (the end-to-end path).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 import threading
 
@@ -34,7 +36,8 @@ EXPORTED = ("wkv7_opts_default", "wkv7_forward", "wkv7_decode_step", "wkv7_works
             "wkv7_backward_static", "wkv7_layer_forward", "wkv7_layer_workspace_bytes", "wkv7_probe_fp32_fma",
             "wkv7_probe_tf32_mma", "wkv7_forward_host", "wkv7_forward_host_workspace_bytes", "wkv7_epilogue",
             "wkv7_epilogue_backward", "wkv7_epilogue_backward_workspace_bytes", "wkv7_decode_step_ex",
-            "wkv7_decode_step_raw")
+            "wkv7_decode_step_raw", "wkv7_delta_opts_default", "wkv7_delta_forward", "wkv7_delta_step",
+            "wkv7_beam_select", "wkv7_beam_select_workspace_bytes", "wkv7_beam_reorder")
 
 
 class Wkv7Error(RuntimeError):
@@ -61,6 +64,12 @@ class Opts(ctypes.Structure):
                 ("snapshots", ctypes.c_void_p), ("ln_w", ctypes.c_void_p), ("ln_b", ctypes.c_void_p),
                 ("r_k", ctypes.c_void_p), ("gn_eps", ctypes.c_float), ("segments", ctypes.c_int),
                 ("handoff_wait_us", ctypes.c_uint), ("withhold_handoff", ctypes.c_int)]
+
+
+class DeltaOpts(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("qk_norm", ctypes.c_int), ("norm_eps", ctypes.c_float),
+                ("cu_seqlens", ctypes.c_void_p), ("q_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong),
+                ("v_stride", ctypes.c_longlong)]
 
 
 _lock = threading.Lock()
@@ -137,6 +146,19 @@ def load():
         lib.wkv7_probe_fp32_fma.restype = ci
         lib.wkv7_probe_tf32_mma.argtypes = [ci, ci, vp, ctypes.POINTER(ctypes.c_double)]
         lib.wkv7_probe_tf32_mma.restype = ci
+        dop, cll, csz = ctypes.POINTER(DeltaOpts), ctypes.c_longlong, ctypes.c_size_t
+        lib.wkv7_delta_opts_default.argtypes = [dop]
+        lib.wkv7_delta_opts_default.restype = None
+        lib.wkv7_delta_forward.argtypes = [ci] * 6 + [vp] * 8 + [dop, vp]
+        lib.wkv7_delta_forward.restype = ci
+        lib.wkv7_delta_step.argtypes = [ci] * 5 + [vp] * 6 + [ci, vp, vp, dop, vp]
+        lib.wkv7_delta_step.restype = ci
+        lib.wkv7_beam_select_workspace_bytes.argtypes = [ci] * 4
+        lib.wkv7_beam_select_workspace_bytes.restype = csz
+        lib.wkv7_beam_select.argtypes = [ci] * 5 + [vp, cll, vp, vp, ci, vp, vp, vp, vp, csz, vp]
+        lib.wkv7_beam_select.restype = ci
+        lib.wkv7_beam_reorder.argtypes = [ci] * 3 + [csz, vp, vp, vp, vp]
+        lib.wkv7_beam_reorder.restype = ci
         if lib.wkv7_abi_version() != ABI_VERSION:
             raise RuntimeError(f"{_LIB_PATH} has ABI version {lib.wkv7_abi_version()}, the binding expects "
                                f"{ABI_VERSION}: rebuild it")
@@ -603,3 +625,175 @@ def forward_host(r, w, k, v, kk, a, S0, y, S_T, workspace, *, algo="auto", chunk
                                    workspace.numel() * workspace.element_size(), _stream_handle(dev, stream))
     _check(st, "wkv7_forward_host")
     return y, S_T, snapshots
+
+
+# ---- gated delta rule, beam search -----------------------------------------------------------------
+
+
+@contextlib.contextmanager
+def _on(dev, stream):
+    """The tensors' device, and `stream` as the current one where the caller names it: what is
+    allocated inside belongs to the stream that the kernels run on."""
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+        else:
+            with torch.cuda.stream(stream):
+                yield ctypes.c_void_p(stream.cuda_stream)
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _plain(name, t, shape, dtype, dev):
+    """A dense tensor of this shape, type and device, or an error that names it."""
+    _need(tuple(t.shape) == tuple(shape), f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    _need(t.device == dev, f"{name} is on {t.device}, expected {dev}")
+    _need(t.is_contiguous(), f"{name} must be contiguous")
+
+
+def _row_stride(name, t, shape, dtype, dev):
+    """Elements from one token's row to the next of a tensor whose heads and channels are dense and
+    whose rows are evenly spaced over all leading dimensions (0 for the dense layout)."""
+    _need(tuple(t.shape) == tuple(shape), f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    _need(t.device == dev, f"{name} is on {t.device}, expected {dev}")
+    if t.is_contiguous():
+        return 0
+    _need((t.shape[-1] == 1 or t.stride(-1) == 1) and (t.shape[-2] == 1 or t.stride(-2) == t.shape[-1]),
+          f"{name} must be dense over its heads and channels")
+    row, step = None, 0
+    for n, st in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        if n == 1:
+            continue
+        if row is None:
+            row, step = st, st
+        _need(st == step, f"{name}: its rows are not evenly spaced; make it contiguous")
+        step *= n
+    return 0 if row is None else row
+
+
+def _delta_args(q, k, v, g, beta, scale, qk_norm, norm_eps, cu_seqlens, lead):
+    """Checks the token tensors (`lead` leading dimensions) and fills the options; returns
+    (rows' leading shape, H, Hk, N, dtype code, options)."""
+    _need(v.dim() == lead + 2, f"v has {v.dim()} dimensions, expected {lead + 2}")
+    _need(k.dim() == lead + 2, f"k has {k.dim()} dimensions, expected {lead + 2}")
+    dt, dev, shape = _dt(v), v.device, tuple(v.shape[:-2])
+    H, N, Hk = v.shape[-2], v.shape[-1], k.shape[-2]
+    o = DeltaOpts()
+    o.q_stride = _row_stride("q", q, (*shape, Hk, N), v.dtype, dev)
+    o.k_stride = _row_stride("k", k, (*shape, Hk, N), v.dtype, dev)
+    o.v_stride = _row_stride("v", v, (*shape, H, N), v.dtype, dev)
+    _plain("g", g, (*shape, H), v.dtype, dev)
+    _plain("beta", beta, (*shape, H), v.dtype, dev)
+    if cu_seqlens is not None:
+        _need(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 2, "cu_seqlens needs at least two entries")
+        _plain("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, dev)
+        o.cu_seqlens = cu_seqlens.data_ptr()
+    o.scale = 0.0 if scale is None else float(scale)
+    o.qk_norm, o.norm_eps = int(qk_norm), float(norm_eps)
+    return shape, H, Hk, N, dt, o
+
+
+def delta_forward(q, k, v, g, beta, S0=None, *, scale=None, qk_norm=False, norm_eps=1e-6, cu_seqlens=None, y=None,
+                  S_T=None, return_state=True, stream=None):
+    """The gated delta rule over sequences (wkv7_delta_forward in include/wkv7.h): q, k
+    [B, T, Hk, N], v [B, T, H, N], g (log decay), beta [B, T, H], bf16 or fp32, or all of them packed
+    ([rows, heads, N], [rows, H]) with cu_seqlens, int32 [B + 1]. Returns (y, S_T): y like v, S_T
+    [B, H, N, N] fp32 (None if return_state is False; may be S0). Rows behind the last packed sequence
+    are not written; without a ``y`` of the caller's they are zeros."""
+    lead = 2 if cu_seqlens is None else 1
+    shape, H, Hk, N, dt, o = _delta_args(q, k, v, g, beta, scale, qk_norm, norm_eps, cu_seqlens, lead)
+    B, T = shape if cu_seqlens is None else (cu_seqlens.numel() - 1, shape[0])
+    dev, states = v.device, (B, H, N, N)
+    if S0 is not None:
+        _plain("S0", S0, states, torch.float32, dev)
+    with _on(dev, stream) as handle:
+        if y is None:
+            y = (torch.empty if cu_seqlens is None else torch.zeros)(v.shape, device=dev, dtype=v.dtype)
+        _plain("y", y, v.shape, v.dtype, dev)
+        if S_T is None and return_state:
+            S_T = torch.empty(states, device=dev, dtype=torch.float32)
+        if S_T is not None:
+            _plain("S_T", S_T, states, torch.float32, dev)
+        st = load().wkv7_delta_forward(B, T, H, Hk, N, dt, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0),
+                                       _ptr(y), _ptr(S_T), ctypes.byref(o), handle)
+    _check(st, "wkv7_delta_forward")
+    return y, S_T
+
+
+def delta_step(q, k, v, g, beta, S, *, slots=None, scale=None, qk_norm=False, norm_eps=1e-6, y=None, stream=None):
+    """One token of the gated delta rule per row (wkv7_delta_step): q, k [B, Hk, N], v [B, H, N], g,
+    beta [B, H]; S [n_slots, H, N, N] fp32 is advanced in place at slots (int32 [B], -1 = padding;
+    None = row b at slot b). Returns y [B, H, N] of the inputs' type, zero for padding."""
+    shape, H, Hk, N, dt, o = _delta_args(q, k, v, g, beta, scale, qk_norm, norm_eps, None, 1)
+    B, dev = shape[0], v.device
+    _need(S.dim() == 4, "S needs four dimensions [n_slots, H, N, N]")
+    _plain("S", S, (S.shape[0], H, N, N), torch.float32, dev)
+    if slots is not None:
+        _plain("slots", slots, (B,), torch.int32, dev)
+    with _on(dev, stream) as handle:
+        if y is None:
+            y = torch.empty(v.shape, device=dev, dtype=v.dtype)
+        _plain("y", y, v.shape, v.dtype, dev)
+        st = load().wkv7_delta_step(B, H, Hk, N, dt, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S),
+                                    S.shape[0], _ptr(slots), _ptr(y), ctypes.byref(o), handle)
+    _check(st, "wkv7_delta_step")
+    return y
+
+
+def beam_select(logits, scores, M, *, finished=None, eos=0, out=None, workspace=None, stream=None):
+    """The M best continuations of each request over its beams and the vocabulary
+    (wkv7_beam_select): logits [B, K, V] bf16 or fp32 (rows may be spaced apart), scores [B, K] fp32,
+    finished [B, K] bool or uint8. Returns (scores, parents, tokens), each [B, M] (fp32, int32,
+    int32), or fills ``out``, three such tensors."""
+    _need(logits.dim() == 3, "logits needs three dimensions [B, K, V]")
+    lib, dev, dt = load(), logits.device, _dt(logits)
+    B, K, V = logits.shape
+    stride = V
+    if not logits.is_contiguous():
+        _need(V == 1 or logits.stride(2) == 1, "logits must be dense over the vocabulary")
+        stride = logits.stride(1) if K > 1 else (logits.stride(0) if B > 1 else V)
+        _need(B == 1 or K == 1 or logits.stride(0) == K * stride, "logits: its rows are not evenly spaced")
+    _plain("scores", scores, (B, K), torch.float32, dev)
+    if finished is not None:
+        _plain("finished", finished, (B, K), torch.bool if finished.dtype == torch.bool else torch.uint8, dev)
+    with _on(dev, stream) as handle:
+        if out is None:
+            out = (torch.empty((B, M), device=dev, dtype=torch.float32),
+                   torch.empty((B, M), device=dev, dtype=torch.int32), torch.empty((B, M), device=dev, dtype=torch.int32))
+        for n, t, d in zip(("scores", "parents", "tokens"), out, (torch.float32, torch.int32, torch.int32)):
+            _plain("out " + n, t, (B, M), d, dev)
+        need = int(lib.wkv7_beam_select_workspace_bytes(B, K, V, M))
+        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+            workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        st = lib.wkv7_beam_select(B, K, V, M, dt, _ptr(logits), stride, _ptr(scores), _ptr(finished), int(eos),
+                                  *(_ptr(t) for t in out), _ptr(workspace), ws_bytes, handle)
+    _check(st, "wkv7_beam_select")
+    return tuple(out)
+
+
+def beam_reorder(parents, state, *, batch_dim=0, out=None, stream=None):
+    """Moves the rows of ``state`` (contiguous, [.., B, K, ..] with B at batch_dim, any type, the
+    bytes of a row a multiple of 16) to the beams that parents [B, K] int32 names, in place or into
+    ``out`` (wkv7_beam_reorder). Returns the reordered tensor."""
+    _need(parents.dim() == 2, "parents needs two dimensions [B, K]")
+    dev, (B, K) = state.device, parents.shape
+    _plain("parents", parents, (B, K), torch.int32, dev)
+    _need(0 <= batch_dim <= state.dim() - 2 and tuple(state.shape[batch_dim:batch_dim + 2]) == (B, K),
+          f"state has shape {tuple(state.shape)}, expected {(B, K)} at dimension {batch_dim}")
+    _need(state.is_contiguous(), "state must be contiguous")
+    dst = state if out is None else out
+    _plain("out", dst, state.shape, state.dtype, dev)
+    L = math.prod(state.shape[:batch_dim])
+    row = math.prod(state.shape[batch_dim + 2:]) * state.element_size()
+    with _on(dev, stream) as handle:
+        st = load().wkv7_beam_reorder(L, B, K, row, _ptr(parents), _ptr(state), _ptr(dst), handle)
+    _check(st, "wkv7_beam_reorder")
+    return dst
