@@ -1,0 +1,386 @@
+// The gated delta rule over whole sequences, 32 tokens at a time. Within a chunk that starts from S,
+// with G the running sums of the log decays, D_ij = exp(G_i - G_j) and unit (or given) q, k:
+//     X = V - exp(G) (K S^T),  E = W X,  W = (I + A)^-1,  A_ij = D_ij beta_j k_i.k_j (j < i)
+//     Y = exp(G) (Q S^T) + P E,  P_ij = scale D_ij beta_j q_i.k_j (j <= i)
+//     S <- exp(G_C) S + (exp(G_C - G) beta E)^T K
+// The rows of S (value channels) never meet, so a warp owns 16 of them and walks the sequence with
+// everything transposed: S [16][N], X^T, E^T and Y^T [16][32] are accumulator fragments, and each is the
+// next product's left operand after a split into bf16 terms. Only K, Q, W and P come from shared memory.
+// Four more warps load the chunks ahead and prepare W and P (delta_mma.cuh); the two groups meet at named
+// barriers, `full` and `empty` per stage.
+// The state keeps fp32's accuracy (three terms wherever it is read or written). A bf16 y is summed from S, P
+// and E in two terms: one would do for gates and keys as they usually are, but where keys repeat the
+// errors e_j alternate in sign and cancel in y, and a P of one term then missed y by four roundings.
+#include "delta_mma.cuh"
+
+#include <type_traits>
+
+namespace wkv7 {
+
+using namespace dm;
+
+namespace {
+
+constexpr int kStages = 3;
+
+template <int NN, int RW, bool F32>
+struct Layout {
+    static constexpr int TI = F32 ? 3 : 1, TP = F32 ? 3 : 2;
+    static constexpr int KB = TI * C * NN * 2;              // keys (and as much for queries)
+    static constexpr int VB = F32 ? 0 : C * RW * 32;        // values of the CTA's rows; y on its way out
+    static constexpr int kK = 0, kQ = KB, kV = 2 * KB, kW = kV + VB, kP = kW + 3 * kTri, kS = kP + TP * kTri;
+    static constexpr int stage = (kS + int(sizeof(Scalars)) + 127) / 128 * 128;
+    static constexpr int total = kStages * stage + int(sizeof(PrepScratch));
+    static constexpr int threads = RW * 32 + kPrep;
+};
+
+__device__ __forceinline__ float load_gate(const float *p) { return __ldg(p); }
+__device__ __forceinline__ float load_gate(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+
+// Index (0 .. C) of the first of a row's 32 tokens whose value is not finite, over the four lanes that
+// hold the row: x[n][r], x[n][r + 1] are tokens 8 n + 2 t, + 1.
+__device__ __forceinline__ int first_bad(const float (&x)[4][4], int r) {
+    int at = C;
+#pragma unroll
+    for (int n = 3; n >= 0; --n)
+#pragma unroll
+        for (int f = 1; f >= 0; --f)
+            if (!isfinite(x[n][r + f])) at = 8 * n + 2 * (threadIdx.x & 3) + f;
+    at = min(at, __shfl_xor_sync(0xffffffffu, at, 1));
+    return min(at, __shfl_xor_sync(0xffffffffu, at, 2));
+}
+__device__ __forceinline__ bool any_bad(const float (&x)[4][4]) {
+    float z = 0.f;
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z = fmaf(x[n][e], 0.f, z);
+    return __any_sync(0xffffffffu, z != 0.f);
+}
+// Tokens from bad[0] (rows g) and bad[1] (rows g + 8) on get v.
+__device__ __forceinline__ void set_from(float (&x)[4][4], const int (&bad)[2], float v) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (8 * n + 2 * int(threadIdx.x & 3) + (e & 1) >= bad[e >> 1]) x[n][e] = v;
+}
+
+template <int NN, int RW, bool F32>
+__global__ void __launch_bounds__(RW * 32 + kPrep, (!F32 && NN == 64) ? 2 : 1) delta_chunk_kernel(const DeltaArgs p) {
+    using L = Layout<NN, RW, F32>;
+    using Tin = std::conditional_t<F32, float, __nv_bfloat16>;
+    constexpr int TI = L::TI, TP = L::TP, TS = F32 ? 3 : 2, NB = NN * 2, TB = C * NB, VNB = RW * 32;
+    extern __shared__ __align__(128) unsigned char sm[];
+    const uint32_t base = smem_addr(sm);
+    constexpr int slices = NN / (16 * RW);
+    const unsigned unit = blockIdx.x / slices;
+    const int row0 = (blockIdx.x % slices) * 16 * RW;           // first value row of the CTA
+    const int s = unit / unsigned(p.H), h = unit % unsigned(p.H), hk = h / (p.H / p.Hk);
+    long long t0, t1;
+    delta_rows(p.cu, p.T, s, t0, t1);
+    const int chunks = int((t1 - t0 + C - 1) / C);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int full = 2, empty = full + kStages, prep_bar = 1;
+
+    if (warp >= RW) {           // ---- preparing warps ----
+        const int tid = threadIdx.x - RW * 32;
+        PrepScratch *ps = reinterpret_cast<PrepScratch *>(sm + kStages * L::stage);
+        const Tin *q = static_cast<const Tin *>(p.q) + size_t(hk) * NN, *k = static_cast<const Tin *>(p.k) + size_t(hk) * NN;
+        const Tin *v = static_cast<const Tin *>(p.v) + size_t(h) * NN + row0;
+        const Tin *gp = static_cast<const Tin *>(p.g) + h, *bp = static_cast<const Tin *>(p.beta) + h;
+        auto load = [&](int c, float &g, float &b) {
+            const uint32_t st = base + (c % kStages) * L::stage;
+            const long long t = t0 + (long long)c * C;
+            const int n = int(min((long long)C, t1 - t));
+            load_tile<NN, F32>(st + L::kK, k, t, n, p.ks, tid, kPrep);
+            load_tile<NN, F32>(st + L::kQ, q, t, n, p.qs, tid, kPrep);
+            if constexpr (!F32) {
+                for (int i = tid; i < C * RW * 2; i += kPrep) {
+                    const int r = i / (RW * 2), cc = i % (RW * 2);
+                    cp16(st + L::kV + tile<VNB>(r, cc), v + (t + (r < n ? r : 0)) * p.vs + 8 * cc, r < n);
+                }
+            }
+            cp_commit();
+            g = 0.f;
+            b = 0.f;
+            if (tid >= 96 && lane < n) {
+                g = delta_clamp(load_gate(gp + (t + lane) * p.H));
+                b = load_gate(bp + (t + lane) * p.H);
+            }
+        };
+        float g, b, gn = 0.f, bn = 0.f;
+        if (chunks > 0) load(0, gn, bn);
+        for (int c = 0; c < chunks; ++c) {
+            g = gn;
+            b = bn;
+            if (c + 1 < chunks) {
+                if (c + 1 >= kStages) bar_sync(empty + (c + 1) % kStages, L::threads);
+                load(c + 1, gn, bn);
+                cp_wait<1>();
+            } else {
+                cp_wait<0>();
+            }
+            bar_sync(prep_bar, kPrep);
+            unsigned char *st = sm + (c % kStages) * L::stage;
+            const uint32_t sa = base + (c % kStages) * L::stage;
+            prepare_chunk<NN, TI, TP>(sa + L::kK, sa + L::kQ, sa + L::kW, sa + L::kP, reinterpret_cast<Scalars *>(st + L::kS), ps,
+                                      p, g, b, c, tid, prep_bar);
+            bar_arrive(full + c % kStages, L::threads);
+        }
+        return;
+    }
+
+    // ---- one warp per 16 value rows ----
+    const int gr = lane >> 2, tc = lane & 3;
+    const int row = row0 + 16 * warp;
+    const size_t so = (size_t(unit) * NN + row) * NN;
+    float S[NN / 8][4];
+#pragma unroll
+    for (int n = 0; n < NN / 8; ++n) {
+        float2 a = make_float2(0, 0), b = a;
+        if (p.S0) {
+            a = __ldg(reinterpret_cast<const float2 *>(p.S0 + so + gr * NN + 8 * n + 2 * tc));
+            b = __ldg(reinterpret_cast<const float2 *>(p.S0 + so + (gr + 8) * NN + 8 * n + 2 * tc));
+        }
+        S[n][0] = a.x; S[n][1] = a.y; S[n][2] = b.x; S[n][3] = b.y;
+    }
+    Tin *y = static_cast<Tin *>(p.y) + size_t(h) * NN + row;
+    const Tin *vrow = static_cast<const Tin *>(p.v) + size_t(h) * NN + row;
+    const size_t ys = size_t(p.H) * NN;
+    for (int c = 0; c < chunks; ++c) {
+        const uint32_t st = base + (c % kStages) * L::stage;
+        const Scalars *sc = reinterpret_cast<const Scalars *>(sm + (c % kStages) * L::stage + L::kS);
+        const long long t = t0 + (long long)c * C;
+        const int n_tok = int(min((long long)C, t1 - t));
+        float X[4][4] = {}, Y[4][4] = {};
+        [[maybe_unused]] float V[4][4];
+        if constexpr (F32) {    // loaded under the products
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 8 * n + 2 * tc + (e & 1);
+                    V[n][e] = i < n_tok ? __ldg(vrow + (t + i) * p.vs + gr + 8 * (e >> 1)) : 0.f;
+                }
+        }
+        bar_sync(full + c % kStages, L::threads);
+        // X^T = S K^T, Y^T = S Q^T
+#pragma unroll
+        for (int ks = 0; ks < NN / 16; ++ks) {
+            uint32_t a[3][4], bk[TI][2][4], bq[TI][2][4];
+            split_a<3>(S[2 * ks], S[2 * ks + 1], a);
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    ldsm4(bk[i][n], addr_b<NB>(st + L::kK + i * TB, 16 * n, ks));
+                    ldsm4(bq[i][n], addr_b<NB>(st + L::kQ + i * TB, 16 * n, ks));
+                }
+#pragma unroll
+            for (int x = 2; x >= 0; --x)
+#pragma unroll
+                for (int z = TI - 1; z >= 0; --z) {
+                    if (x + z > 2) continue;
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) mma(X[n], a[x], bk[z][n >> 1][2 * (n & 1)], bk[z][n >> 1][2 * (n & 1) + 1]);
+                }
+#pragma unroll
+            for (int x = TS - 1; x >= 0; --x)
+#pragma unroll
+                for (int z = TI - 1; z >= 0; --z) {
+                    if (x + z > TS - 1) continue;
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) mma(Y[n], a[x], bq[z][n >> 1][2 * (n & 1)], bq[z][n >> 1][2 * (n & 1) + 1]);
+                }
+        }
+        if constexpr (!F32) {   // the values, transposed on the way: tokens 2 t, 2 t + 1 of rows g and g + 8
+            uint32_t r[2][4];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int tok = 16 * m + (lane & 7) + ((lane >> 4) << 3);
+                ldsm4t(r[m], st + L::kV + tile<VNB>(tok, 2 * warp + ((lane >> 3) & 1)));
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                V[n][0] = lo_f(r[n >> 1][2 * (n & 1)]);
+                V[n][1] = hi_f(r[n >> 1][2 * (n & 1)]);
+                V[n][2] = lo_f(r[n >> 1][2 * (n & 1) + 1]);
+                V[n][3] = hi_f(r[n >> 1][2 * (n & 1) + 1]);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const float2 in = *reinterpret_cast<const float2 *>(&sc->kin[8 * n + 2 * tc]);
+            const float2 qn = *reinterpret_cast<const float2 *>(&sc->qin[8 * n + 2 * tc]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                X[n][e] = fmaf(-(e & 1 ? in.y : in.x), X[n][e], V[n][e]);
+                Y[n][e] *= e & 1 ? qn.y : qn.x;
+            }
+        }
+        // A value that is not finite makes its row so from its token on and no earlier, which products
+        // with the zeros of W and P would not keep: such tokens leave the products and are set afterwards.
+        int bad[2] = {C, C};
+        bool poisoned = false;                  // the same in every lane of the warp
+        if (any_bad(X)) {
+            poisoned = true;
+            bad[0] = first_bad(X, 0);
+            bad[1] = first_bad(X, 2);
+            set_from(X, bad, 0.f);
+        }
+        // E^T = X^T W^T
+        float E[4][4] = {};
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            uint32_t a[3][4];
+            split_a<3>(X[2 * kb], X[2 * kb + 1], a);
+#pragma unroll
+            for (int ib = kb; ib < 2; ++ib) {
+                uint32_t w[3][4];
+#pragma unroll
+                for (int z = 0; z < 3; ++z) ldsm4(w[z], addr_block(st + L::kW + z * kTri + (ib + kb) * 512));
+#pragma unroll
+                for (int x = 2; x >= 0; --x)
+#pragma unroll
+                    for (int z = 2 - x; z >= 0; --z) {
+                        mma(E[2 * ib], a[x], w[z][0], w[z][1]);
+                        mma(E[2 * ib + 1], a[x], w[z][2], w[z][3]);
+                    }
+            }
+        }
+        if (any_bad(E)) {
+            poisoned = true;
+            bad[0] = min(bad[0], first_bad(E, 0));
+            bad[1] = min(bad[1], first_bad(E, 2));
+            set_from(E, bad, 0.f);
+        }
+        // Y^T += E^T P^T
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            uint32_t a[TS][4];
+            split_a<TS>(E[2 * kb], E[2 * kb + 1], a);
+#pragma unroll
+            for (int ib = kb; ib < 2; ++ib) {
+                uint32_t w[TP][4];
+#pragma unroll
+                for (int z = 0; z < TP; ++z) ldsm4(w[z], addr_block(st + L::kP + z * kTri + (ib + kb) * 512));
+#pragma unroll
+                for (int x = TS - 1; x >= 0; --x)
+#pragma unroll
+                    for (int z = TP - 1; z >= 0; --z) {
+                        if (x + z > TS - 1) continue;
+                        mma(Y[2 * ib], a[x], w[z][0], w[z][1]);
+                        mma(Y[2 * ib + 1], a[x], w[z][2], w[z][3]);
+                    }
+            }
+        }
+        // S <- exp(G_C) S + U^T K, U = out E
+        const float whole = sc->whole;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const float2 o = *reinterpret_cast<const float2 *>(&sc->out[8 * n + 2 * tc]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) E[n][e] *= e & 1 ? o.y : o.x;
+        }
+#pragma unroll
+        for (int n = 0; n < NN / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[n][e] *= whole;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            uint32_t a[3][4];
+            split_a<3>(E[2 * kb], E[2 * kb + 1], a);
+#pragma unroll
+            for (int n = 0; n < NN / 16; ++n) {
+                uint32_t b[TI][4];
+#pragma unroll
+                for (int z = 0; z < TI; ++z) ldsm4t(b[z], addr_bt<NB>(st + L::kK + z * TB, 16 * kb, 2 * n));
+#pragma unroll
+                for (int x = 2; x >= 0; --x)
+#pragma unroll
+                    for (int z = TI - 1; z >= 0; --z) {
+                        if (x + z > 2) continue;
+                        mma(S[2 * n], a[x], b[z][0], b[z][1]);
+                        mma(S[2 * n + 1], a[x], b[z][2], b[z][3]);
+                    }
+            }
+        }
+        if (poisoned) {
+            const float nan = __int_as_float(0x7fffffff);
+            set_from(Y, bad, nan);
+#pragma unroll
+            for (int n = 0; n < NN / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (bad[e >> 1] < C) S[n][e] = nan;
+        }
+        if constexpr (F32) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 8 * n + 2 * tc + (e & 1);
+                    if (i < n_tok) y[(t + i) * ys + gr + 8 * (e >> 1)] = Y[n][e];
+                }
+        } else {                // through the values' place (this warp's own columns) to whole 32-byte pieces
+            __syncwarp();
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                uint32_t r[4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    r[2 * i] = pack(Y[2 * m + i][0], Y[2 * m + i][1]);
+                    r[2 * i + 1] = pack(Y[2 * m + i][2], Y[2 * m + i][3]);
+                }
+                const int tok = 16 * m + (lane & 7) + ((lane >> 4) << 3);
+                stsm4t(st + L::kV + tile<VNB>(tok, 2 * warp + ((lane >> 3) & 1)), r);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int tok = 16 * m + (lane >> 1);
+                uint4 r;
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                             : "r"(st + L::kV + tile<VNB>(tok, 2 * warp + (lane & 1))) : "memory");
+                if (tok < n_tok) *reinterpret_cast<uint4 *>(y + (t + tok) * ys + 8 * (lane & 1)) = r;
+            }
+        }
+        if (c + kStages < chunks) bar_arrive(empty + c % kStages, L::threads);
+    }
+    if (p.S_T) {
+#pragma unroll
+        for (int n = 0; n < NN / 8; ++n) {
+            *reinterpret_cast<float2 *>(p.S_T + so + gr * NN + 8 * n + 2 * tc) = make_float2(S[n][0], S[n][1]);
+            *reinterpret_cast<float2 *>(p.S_T + so + (gr + 8) * NN + 8 * n + 2 * tc) = make_float2(S[n][2], S[n][3]);
+        }
+    }
+}
+
+}  // namespace
+
+// ---- host side ---------------------------------------------------------------------------------------
+
+cudaError_t allow_dynamic_smem(const void *kernel, int bytes);
+
+namespace {
+
+template <int NN, int RW, bool F32>
+cudaError_t launch_t(const DeltaArgs &p) {
+    using L = Layout<NN, RW, F32>;
+    const void *kernel = reinterpret_cast<const void *>(delta_chunk_kernel<NN, RW, F32>);
+    const cudaError_t e = allow_dynamic_smem(kernel, L::total);
+    if (e != cudaSuccess) return e;
+    delta_chunk_kernel<NN, RW, F32><<<unsigned(p.B) * p.H * (NN / (16 * RW)), L::threads, L::total, p.stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_delta_forward(const DeltaArgs &p) {
+    const bool f32 = p.dt == WKV7_F32;
+    if (p.N == 64) return f32 ? launch_t<64, 4, true>(p) : launch_t<64, 4, false>(p);
+    return f32 ? launch_t<128, 4, true>(p) : launch_t<128, 8, false>(p);
+}
+
+}  // namespace wkv7
