@@ -6,8 +6,8 @@
 // The rows of S (value channels) never meet, so a warp owns 16 of them and walks the sequence with
 // everything transposed: S [16][N], X^T, E^T and Y^T [16][32] are accumulator fragments, and each is the
 // next product's left operand after a split into bf16 terms. Only K, Q, W and P come from shared memory.
-// Four more warps load the chunks ahead and prepare W and P (delta_mma.cuh); the two groups meet at named
-// barriers, `full` and `empty` per stage.
+// Four more warps load the chunks ahead and prepare W and P (delta_mma.cuh), two to a chunk; they meet the
+// others at named barriers, `full` and `empty` per stage.
 // The state keeps fp32's accuracy (three terms wherever it is read or written). A bf16 y is summed from S, P
 // and E in two terms: one would do for gates and keys as they usually are, but where keys repeat the
 // errors e_j alternate in sign and cancel in y, and a P of one term then missed y by four roundings.
@@ -21,8 +21,6 @@ using namespace dm;
 
 namespace {
 
-constexpr int kStages = 3;
-
 template <int NN, int RW, bool F32>
 struct Layout {
     static constexpr int TI = F32 ? 3 : 1, TP = F32 ? 3 : 2;
@@ -30,44 +28,39 @@ struct Layout {
     static constexpr int VB = F32 ? 0 : C * RW * 32;        // values of the CTA's rows; y on its way out
     static constexpr int kK = 0, kQ = KB, kV = 2 * KB, kW = kV + VB, kP = kW + 3 * kTri, kS = kP + TP * kTri;
     static constexpr int stage = (kS + int(sizeof(Scalars)) + 127) / 128 * 128;
-    static constexpr int total = kStages * stage + int(sizeof(PrepScratch));
-    static constexpr int threads = RW * 32 + kPrep;
+    // two chunks being prepared, one at work, and the rest loading: what two CTAs of N = 64 bf16, or one of
+    // the others, have room for
+    static constexpr int stages = F32 ? (NN == 64 ? 6 : 3) : (NN == 64 ? 5 : 6);
+    static constexpr int total = stages * stage + kGroups * int(sizeof(PrepScratch));
+    static constexpr int threads = RW * 32 + kGroups * kGroup, meet = RW * 32 + kGroup;
 };
 
-__device__ __forceinline__ float load_gate(const float *p) { return __ldg(p); }
-__device__ __forceinline__ float load_gate(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
-
-// Index (0 .. C) of the first of a row's 32 tokens whose value is not finite, over the four lanes that
-// hold the row: x[n][r], x[n][r + 1] are tokens 8 n + 2 t, + 1.
-__device__ __forceinline__ int first_bad(const float (&x)[4][4], int r) {
+// Values that are not finite leave the products (0) and their places the mask: bit 4 n + e.
+__device__ __forceinline__ void take_out(float (&x)[4][4], uint32_t &mask) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool ok = fabsf(x[n][e]) < INFINITY;
+            mask |= ok ? 0u : 1u << (4 * n + e);
+            x[n][e] = ok ? x[n][e] : 0.f;
+        }
+}
+// Index (0 .. C) of the first such token of the row that holds elements r, r + 1 of this lane's tiles
+// (tokens 8 n + 2 t, + 1), over the four lanes of the row.
+__device__ __forceinline__ int first_bad(uint32_t mask, int r) {
     int at = C;
 #pragma unroll
     for (int n = 3; n >= 0; --n)
 #pragma unroll
         for (int f = 1; f >= 0; --f)
-            if (!isfinite(x[n][r + f])) at = 8 * n + 2 * (threadIdx.x & 3) + f;
+            if (mask >> (4 * n + r + f) & 1) at = 8 * n + 2 * (threadIdx.x & 3) + f;
     at = min(at, __shfl_xor_sync(0xffffffffu, at, 1));
     return min(at, __shfl_xor_sync(0xffffffffu, at, 2));
 }
-__device__ __forceinline__ bool any_bad(const float (&x)[4][4]) {
-    float z = 0.f;
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) z = fmaf(x[n][e], 0.f, z);
-    return __any_sync(0xffffffffu, z != 0.f);
-}
-// Tokens from bad[0] (rows g) and bad[1] (rows g + 8) on get v.
-__device__ __forceinline__ void set_from(float (&x)[4][4], const int (&bad)[2], float v) {
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (8 * n + 2 * int(threadIdx.x & 3) + (e & 1) >= bad[e >> 1]) x[n][e] = v;
-}
 
 template <int NN, int RW, bool F32>
-__global__ void __launch_bounds__(RW * 32 + kPrep, (!F32 && NN == 64) ? 2 : 1) delta_chunk_kernel(const DeltaArgs p) {
+__global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64) ? 2 : 1) delta_chunk_kernel(const DeltaArgs p) {
     using L = Layout<NN, RW, F32>;
     using Tin = std::conditional_t<F32, float, __nv_bfloat16>;
     constexpr int TI = L::TI, TP = L::TP, TS = F32 ? 3 : 2, NB = NN * 2, TB = C * NB, VNB = RW * 32;
@@ -81,52 +74,45 @@ __global__ void __launch_bounds__(RW * 32 + kPrep, (!F32 && NN == 64) ? 2 : 1) d
     delta_rows(p.cu, p.T, s, t0, t1);
     const int chunks = int((t1 - t0 + C - 1) / C);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int full = 2, empty = full + kStages, prep_bar = 1;
+    constexpr int full = 1 + kGroups, empty = full + L::stages;      // named barriers; 1 .. kGroups: the groups' own
 
-    if (warp >= RW) {           // ---- preparing warps ----
-        const int tid = threadIdx.x - RW * 32;
-        PrepScratch *ps = reinterpret_cast<PrepScratch *>(sm + kStages * L::stage);
-        const Tin *q = static_cast<const Tin *>(p.q) + size_t(hk) * NN, *k = static_cast<const Tin *>(p.k) + size_t(hk) * NN;
-        const Tin *v = static_cast<const Tin *>(p.v) + size_t(h) * NN + row0;
-        const Tin *gp = static_cast<const Tin *>(p.g) + h, *bp = static_cast<const Tin *>(p.beta) + h;
-        auto load = [&](int c, float &g, float &b) {
-            const uint32_t st = base + (c % kStages) * L::stage;
-            const long long t = t0 + (long long)c * C;
-            const int n = int(min((long long)C, t1 - t));
-            load_tile<NN, F32>(st + L::kK, k, t, n, p.ks, tid, kPrep);
-            load_tile<NN, F32>(st + L::kQ, q, t, n, p.qs, tid, kPrep);
-            if constexpr (!F32) {
-                for (int i = tid; i < C * RW * 2; i += kPrep) {
-                    const int r = i / (RW * 2), cc = i % (RW * 2);
-                    cp16(st + L::kV + tile<VNB>(r, cc), v + (t + (r < n ? r : 0)) * p.vs + 8 * cc, r < n);
-                }
-            }
+    if (warp >= RW) {           // ---- preparing warps: group g takes chunks g, g + kGroups, ... ----
+        const int group = (warp - RW) >> 1, tid = (threadIdx.x - RW * 32) % kGroup;
+        PrepScratch *ps = reinterpret_cast<PrepScratch *>(sm + L::stages * L::stage) + group;
+        RowLoader<NN, F32> k(p.k, t0 + group * C, (long long)hk * NN, p.ks, tid), q(p.q, t0 + group * C, (long long)hk * NN, p.qs, tid);
+        RowLoader<RW * 16, F32> v(p.v, t0 + group * C, (long long)h * NN + row0, p.vs, tid);
+        Gate<F32> gate, next{};
+        auto load = [&](int c) {
+            const uint32_t st = base + (c % L::stages) * L::stage;
+            const int n = int(min((long long)C, t1 - t0 - (long long)c * C));
+            next.load(p.g, p.beta, (t0 + (long long)c * C + lane) * p.H + h, lane < n);
+            k.load(st + L::kK, n);
+            q.load(st + L::kQ, n);
+            if constexpr (!F32) v.load(st + L::kV, n);
+            k.advance(kGroups);
+            q.advance(kGroups);
+            v.advance(kGroups);
             cp_commit();
-            g = 0.f;
-            b = 0.f;
-            if (tid >= 96 && lane < n) {
-                g = delta_clamp(load_gate(gp + (t + lane) * p.H));
-                b = load_gate(bp + (t + lane) * p.H);
-            }
         };
-        float g, b, gn = 0.f, bn = 0.f;
-        if (chunks > 0) load(0, gn, bn);
-        for (int c = 0; c < chunks; ++c) {
-            g = gn;
-            b = bn;
-            if (c + 1 < chunks) {
-                if (c + 1 >= kStages) bar_sync(empty + (c + 1) % kStages, L::threads);
-                load(c + 1, gn, bn);
+        if (group < chunks) load(group);
+        for (int c = group; c < chunks; c += kGroups) {
+            gate = next;
+            if (c + kGroups < chunks) {
+                if (c + kGroups >= L::stages) bar_sync(empty + (c + kGroups) % L::stages, L::meet);
+                load(c + kGroups);
                 cp_wait<1>();
             } else {
                 cp_wait<0>();
             }
-            bar_sync(prep_bar, kPrep);
-            unsigned char *st = sm + (c % kStages) * L::stage;
-            const uint32_t sa = base + (c % kStages) * L::stage;
-            prepare_chunk<NN, TI, TP>(sa + L::kK, sa + L::kQ, sa + L::kW, sa + L::kP, reinterpret_cast<Scalars *>(st + L::kS), ps,
-                                      p, g, b, c, tid, prep_bar);
-            bar_arrive(full + c % kStages, L::threads);
+            bar_sync(1 + group, kGroup);
+            unsigned char *st = sm + (c % L::stages) * L::stage;
+            const uint32_t sa = base + (c % L::stages) * L::stage;
+            // the longer of the two roles changes between the warps, and with them the schedulers
+            const bool queries = ((warp ^ (c / kGroups)) & 1) != 0;
+            Scalars *sc = reinterpret_cast<Scalars *>(st + L::kS);
+            const float g = delta_clamp(gate.num(gate.g)), bt = gate.num(gate.beta);
+            prepare_chunk<NN, TI, TP>(sa + L::kK, sa + L::kQ, sa + L::kW, sa + L::kP, sc, ps, p, g, bt, queries, 1 + group);
+            bar_arrive(full + c % L::stages, L::meet);
         }
         return;
     }
@@ -149,12 +135,13 @@ __global__ void __launch_bounds__(RW * 32 + kPrep, (!F32 && NN == 64) ? 2 : 1) d
     const Tin *vrow = static_cast<const Tin *>(p.v) + size_t(h) * NN + row;
     const size_t ys = size_t(p.H) * NN;
     for (int c = 0; c < chunks; ++c) {
-        const uint32_t st = base + (c % kStages) * L::stage;
-        const Scalars *sc = reinterpret_cast<const Scalars *>(sm + (c % kStages) * L::stage + L::kS);
+        const uint32_t st = base + (c % L::stages) * L::stage;
+        const Scalars *sc = reinterpret_cast<const Scalars *>(sm + (c % L::stages) * L::stage + L::kS);
         const long long t = t0 + (long long)c * C;
         const int n_tok = int(min((long long)C, t1 - t));
         float X[4][4] = {}, Y[4][4] = {};
         [[maybe_unused]] float V[4][4];
+        [[maybe_unused]] uint32_t vraw[2][4];
         if constexpr (F32) {    // loaded under the products
 #pragma unroll
             for (int n = 0; n < 4; ++n)
@@ -164,49 +151,66 @@ __global__ void __launch_bounds__(RW * 32 + kPrep, (!F32 && NN == 64) ? 2 : 1) d
                     V[n][e] = i < n_tok ? __ldg(vrow + (t + i) * p.vs + gr + 8 * (e >> 1)) : 0.f;
                 }
         }
-        bar_sync(full + c % kStages, L::threads);
+        bar_sync(full + c % L::stages, L::meet);
+        float z = 0.f;
+        if constexpr (!F32) {   // the values, transposed on the way: tokens 2 t, 2 t + 1 of rows g and g + 8
+            __nv_bfloat162 zz = __float2bfloat162_rn(0.f);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int tok = 16 * m + (lane & 7) + ((lane >> 4) << 3);
+                ldsm4t(vraw[m], st + L::kV + tile<VNB>(tok, 2 * warp + ((lane >> 3) & 1)));
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    zz = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&vraw[m][i]), __float2bfloat162_rn(0.f), zz);
+            }
+            z = __low2float(zz) + __high2float(zz);
+        } else {
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z = fmaf(V[n][e], 0.f, z);
+        }
+        // A value that is not finite makes its row so from its token on and no earlier, which products with
+        // the zeros of W and P would not keep. In a chunk with such inputs (NaN or infinite v, k, g or beta)
+        // such values are taken out of the products, and what follows them is set at the end.
+        const bool careful = sc->odd || __any_sync(0xffffffffu, z != 0.f);       // the same in every lane
         // X^T = S K^T, Y^T = S Q^T
 #pragma unroll
         for (int ks = 0; ks < NN / 16; ++ks) {
-            uint32_t a[3][4], bk[TI][2][4], bq[TI][2][4];
+            uint32_t a[3][4], b[TI][2][4];
             split_a<3>(S[2 * ks], S[2 * ks + 1], a);
 #pragma unroll
             for (int i = 0; i < TI; ++i)
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    ldsm4(bk[i][n], addr_b<NB>(st + L::kK + i * TB, 16 * n, ks));
-                    ldsm4(bq[i][n], addr_b<NB>(st + L::kQ + i * TB, 16 * n, ks));
-                }
+                for (int n = 0; n < 2; ++n) ldsm4(b[i][n], addr_b<NB>(st + L::kK + i * TB, 16 * n, ks));
 #pragma unroll
             for (int x = 2; x >= 0; --x)
 #pragma unroll
                 for (int z = TI - 1; z >= 0; --z) {
                     if (x + z > 2) continue;
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) mma(X[n], a[x], bk[z][n >> 1][2 * (n & 1)], bk[z][n >> 1][2 * (n & 1) + 1]);
+                    for (int n = 0; n < 4; ++n) mma(X[n], a[x], b[z][n >> 1][2 * (n & 1)], b[z][n >> 1][2 * (n & 1) + 1]);
                 }
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) ldsm4(b[i][n], addr_b<NB>(st + L::kQ + i * TB, 16 * n, ks));
 #pragma unroll
             for (int x = TS - 1; x >= 0; --x)
 #pragma unroll
                 for (int z = TI - 1; z >= 0; --z) {
                     if (x + z > TS - 1) continue;
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) mma(Y[n], a[x], bq[z][n >> 1][2 * (n & 1)], bq[z][n >> 1][2 * (n & 1) + 1]);
+                    for (int n = 0; n < 4; ++n) mma(Y[n], a[x], b[z][n >> 1][2 * (n & 1)], b[z][n >> 1][2 * (n & 1) + 1]);
                 }
         }
-        if constexpr (!F32) {   // the values, transposed on the way: tokens 2 t, 2 t + 1 of rows g and g + 8
-            uint32_t r[2][4];
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int tok = 16 * m + (lane & 7) + ((lane >> 4) << 3);
-                ldsm4t(r[m], st + L::kV + tile<VNB>(tok, 2 * warp + ((lane >> 3) & 1)));
-            }
+        if constexpr (!F32) {
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                V[n][0] = lo_f(r[n >> 1][2 * (n & 1)]);
-                V[n][1] = hi_f(r[n >> 1][2 * (n & 1)]);
-                V[n][2] = lo_f(r[n >> 1][2 * (n & 1) + 1]);
-                V[n][3] = hi_f(r[n >> 1][2 * (n & 1) + 1]);
+                V[n][0] = lo_f(vraw[n >> 1][2 * (n & 1)]);
+                V[n][1] = hi_f(vraw[n >> 1][2 * (n & 1)]);
+                V[n][2] = lo_f(vraw[n >> 1][2 * (n & 1) + 1]);
+                V[n][3] = hi_f(vraw[n >> 1][2 * (n & 1) + 1]);
             }
         }
 #pragma unroll
@@ -219,16 +223,8 @@ __global__ void __launch_bounds__(RW * 32 + kPrep, (!F32 && NN == 64) ? 2 : 1) d
                 Y[n][e] *= e & 1 ? qn.y : qn.x;
             }
         }
-        // A value that is not finite makes its row so from its token on and no earlier, which products
-        // with the zeros of W and P would not keep: such tokens leave the products and are set afterwards.
-        int bad[2] = {C, C};
-        bool poisoned = false;                  // the same in every lane of the warp
-        if (any_bad(X)) {
-            poisoned = true;
-            bad[0] = first_bad(X, 0);
-            bad[1] = first_bad(X, 2);
-            set_from(X, bad, 0.f);
-        }
+        uint32_t bad = 0;
+        if (careful) take_out(X, bad);
         // E^T = X^T W^T
         float E[4][4] = {};
 #pragma unroll
@@ -249,12 +245,7 @@ __global__ void __launch_bounds__(RW * 32 + kPrep, (!F32 && NN == 64) ? 2 : 1) d
                     }
             }
         }
-        if (any_bad(E)) {
-            poisoned = true;
-            bad[0] = min(bad[0], first_bad(E, 0));
-            bad[1] = min(bad[1], first_bad(E, 2));
-            set_from(E, bad, 0.f);
-        }
+        if (careful) take_out(E, bad);
         // Y^T += E^T P^T
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
@@ -306,14 +297,19 @@ __global__ void __launch_bounds__(RW * 32 + kPrep, (!F32 && NN == 64) ? 2 : 1) d
                     }
             }
         }
-        if (poisoned) {
+        if (careful) {
             const float nan = __int_as_float(0x7fffffff);
-            set_from(Y, bad, nan);
+            const int from[2] = {first_bad(bad, 0), first_bad(bad, 2)};
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (8 * n + 2 * tc + (e & 1) >= from[e >> 1]) Y[n][e] = nan;
 #pragma unroll
             for (int n = 0; n < NN / 8; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (bad[e >> 1] < C) S[n][e] = nan;
+                    if (from[e >> 1] < C) S[n][e] = nan;
         }
         if constexpr (F32) {
 #pragma unroll
@@ -346,7 +342,7 @@ __global__ void __launch_bounds__(RW * 32 + kPrep, (!F32 && NN == 64) ? 2 : 1) d
                 if (tok < n_tok) *reinterpret_cast<uint4 *>(y + (t + tok) * ys + 8 * (lane & 1)) = r;
             }
         }
-        if (c + kStages < chunks) bar_arrive(empty + c % kStages, L::threads);
+        if (c + L::stages < chunks) bar_arrive(empty + c % L::stages, L::meet);
     }
     if (p.S_T) {
 #pragma unroll

@@ -13,15 +13,18 @@
 // the pairs (a, b) with a + b < the larger count, and sums are fp32. bf16 inputs are one exact term.
 #pragma once
 
+#include <type_traits>
+
 #include "delta.cuh"
 
 namespace wkv7 {
 namespace dm {
 
 constexpr int C = 32;               // tokens per chunk
-constexpr int kPrep = 128;          // threads that prepare chunks
+constexpr int kGroup = 64;          // threads that prepare one chunk: a warp for the keys, one for the queries
+constexpr int kGroups = 2;          // chunks prepared at a time
 constexpr int kTri = 3 * 512;       // bytes of one term of a lower triangular [32][32]: blocks (0,0), (1,0), (1,1)
-constexpr int kAs = 36;             // row of the fp32 scratch matrix
+constexpr int kAs = 20;             // row of a 16 x 16 fp32 scratch block
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -51,6 +54,12 @@ template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.as
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory"); }
 __device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" :: "r"(id), "r"(threads) : "memory"); }
 
+__device__ __forceinline__ void st_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+__device__ __forceinline__ void st_b32(uint32_t a, uint32_t x) { asm volatile("st.shared.b32 [%0], %1;" :: "r"(a), "r"(x) : "memory"); }
+
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 __device__ __forceinline__ uint32_t pack(float x, float y) {      // x in the low half
@@ -58,16 +67,18 @@ __device__ __forceinline__ uint32_t pack(float x, float y) {      // x in the lo
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(y), "f"(x));
     return u;
 }
-// Two values as T bf16 terms each: r[0] the values rounded, r[1] what that left, rounded, and so on.
+// Two values as T bf16 terms each: r[0] the values rounded, r[1] what that left, rounded, and so on. The
+// remainder is one mixed-precision multiply-add per value (x - hi), without unpacking hi first: 13.6
+// against 16.3 issue slots for a split with its surroundings, same bits.
 template <int T>
-__device__ __forceinline__ void split2(float x, float y, uint32_t *r, int step = 1) {
+__device__ __forceinline__ void split2(float x, float y, uint32_t *r) {
 #pragma unroll
     for (int i = 0; i < T; ++i) {
-        r[i * step] = pack(x, y);
-        if (i + 1 < T) {
-            x -= lo_f(r[i * step]);
-            y -= hi_f(r[i * step]);
-        }
+        r[i] = pack(x, y);
+        if (i + 1 < T)
+            asm("{\n\t.reg .b16 l, h, m;\n\tmov.b16 m, 0xBF80;\n\tmov.b32 {l, h}, %2;\n\t"
+                "fma.rn.f32.bf16 %0, l, m, %0;\n\tfma.rn.f32.bf16 %1, h, m, %1;\n\t}"
+                : "+f"(x), "+f"(y) : "r"(r[i]));
     }
 }
 // The accumulators of two neighbouring 16 x 8 tiles as the left operand of a 16-deep product, T terms.
@@ -123,199 +134,316 @@ struct Scalars {
     float kout[C];   // exp(G_C - G_j) / |k_j| (backward)
     float beta[C];
     float whole;     // exp(G_C)
-    float pad[3];
+    int odd;         // a key or gate of the chunk is not finite (or a gate grows beyond fp32)
+    float pad[2];
 };
 
-// Scratch of the preparing threads.
+// Scratch of one preparing group.
 struct PrepScratch {
-    float A[C * kAs];
-    float T[C * kAs];
-    float ghi[C], glo[C], rk[C], rq[C];
+    float A[2][16 * kAs + 16];      // the diagonal blocks of A by columns, then of W by rows
+    float rk[C], rq[C];
 };
 
-// Rows [t0, t0 + C) of a strided tensor into TI tiles of bf16 terms; rows from `n` on are zero.
-// bf16: asynchronous copies (the caller commits and waits). fp32: loaded, split and stored.
-template <int NN, bool F32>
-__device__ __forceinline__ void load_tile(uint32_t dst, const void *src, long long t0, int n, long long stride, int tid, int threads) {
-    if constexpr (!F32) {
-        const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(src);
-        for (int i = tid; i < C * NN / 8; i += threads) {
-            const int r = i / (NN / 8), c = i % (NN / 8);
-            cp16(dst + tile<NN * 2>(r, c), p + (t0 + (r < n ? r : 0)) * stride + 8 * c, r < n);
-        }
-    } else {
-        const float *p = static_cast<const float *>(src);
-        for (int i = tid; i < C * NN / 8; i += threads) {
-            const int r = i / (NN / 8), c = i % (NN / 8);
-            float4 x = make_float4(0, 0, 0, 0), y = x;
-            if (r < n) {
-                const float4 *q = reinterpret_cast<const float4 *>(p + (t0 + r) * stride + 8 * c);
-                x = __ldg(q);
-                y = __ldg(q + 1);
-            }
-            uint32_t w[4][3];
-            split2<3>(x.x, x.y, w[0]);
-            split2<3>(x.z, x.w, w[1]);
-            split2<3>(y.x, y.y, w[2]);
-            split2<3>(y.z, y.w, w[3]);
+// One strided tensor's rows on their way to the tiles of a stage, by one preparing group: a thread keeps
+// one 16-byte column (fp32: 32 bytes) of every STEP-th row.
+template <int W, bool F32>
+struct RowLoader {
+    static constexpr int CH = W / 8, STEP = kGroup / CH, N = C / STEP;   // STEP rows at a time
+    using Tin = std::conditional_t<F32, float, __nv_bfloat16>;
+    const Tin *at, *safe;            // safe: an address inside the tensor for copies of no bytes
+    long long stride;
+    int r, c;
+    __device__ __forceinline__ RowLoader(const void *base, long long first, long long offset, long long row_stride, int tid) {
+        r = tid / CH;
+        c = tid % CH;
+        stride = row_stride;
+        safe = static_cast<const Tin *>(base);
+        at = static_cast<const Tin *>(base) + offset + (first + r) * row_stride + 8 * c;
+    }
+    // Moves on by so many chunks of C rows (or back).
+    __device__ __forceinline__ void advance(int chunks) { at += chunks * (C * stride); }
+    // C rows from the current ones on; rows from n on become zeros. bf16: asynchronous (the caller commits).
+    __device__ __forceinline__ void load(uint32_t dst, int n) const {
+        const Tin *p = at;
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                const uint32_t at = dst + k * (C * NN * 2) + tile<NN * 2>(r, c);
-                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(at), "r"(w[0][k]), "r"(w[1][k]), "r"(w[2][k]), "r"(w[3][k]) : "memory");
+        for (int i = 0; i < N; ++i, p += STEP * stride) {
+            const bool there = r + i * STEP < n;
+            const uint32_t to = dst + tile<W * 2>(r + i * STEP, c);
+            if constexpr (!F32) {
+                cp16(to, there ? p : safe, there);
+            } else {
+                float4 x = make_float4(0, 0, 0, 0), y = x;
+                if (there) {
+                    x = __ldg(reinterpret_cast<const float4 *>(p));
+                    y = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+                }
+                uint32_t w[4][3];
+                split2<3>(x.x, x.y, w[0]);
+                split2<3>(x.z, x.w, w[1]);
+                split2<3>(y.x, y.y, w[2]);
+                split2<3>(y.z, y.w, w[3]);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) st_v4(to + k * (C * W * 2), w[0][k], w[1][k], w[2][k], w[3][k]);
             }
         }
     }
-}
+};
 
-// The state-free part of one chunk, by the kPrep preparing threads (thread index tid, named barrier
+// A token's gates as loaded; turned into numbers only when the chunk is prepared, so that nothing waits.
+template <bool F32> struct Gate {
+    using T = std::conditional_t<F32, float, unsigned short>;
+    T g, beta;
+    __device__ __forceinline__ void load(const void *gp, const void *bp, long long at, bool there) {
+        g = beta = T(0);
+        if (there) {
+            g = __ldg(static_cast<const T *>(gp) + at);
+            beta = __ldg(static_cast<const T *>(bp) + at);
+        }
+    }
+    static __device__ __forceinline__ float num(T x) {
+        if constexpr (F32) return x;
+        else return __uint_as_float(uint32_t(x) << 16);
+    }
+};
+
+// exp for decays between tokens: two instructions, relative error about 1e-7 + 6e-8 |x|, so the decays
+// that weigh anything keep fp32's accuracy.
+__device__ __forceinline__ float fast_exp(float x) { return __expf(x); }
+
+// The state-free part of one chunk, by a group of two warps (`queries`: this warp's role; named barrier
 // `bar`). With D_ij = exp(G_i - G_j) and unit or given q, k:
-//     P_ij = scale D_ij beta_j q_i.k_j  (j <= i)         -> TP terms
-//     W = (I + A)^-1, A_ij = D_ij beta_j k_i.k_j (j < i)  -> 3 terms
-// k, q: TI tiles of bf16 terms; g, beta: this thread's token (lanes of the last warp), 0 behind the end.
-// The sums G are taken in fp64 and kept as two floats (the first a multiple of 2^-10), so that differences
-// of large sums keep their low bits. W comes from forward substitution by one warp, a column per lane, in
-// fp32 (496 products); the warp changes with the chunk so that no scheduler gets all of it.
+//     P_ij = scale D_ij beta_j q_i.k_j  (j <= i)         -> TP terms       (the warp of the queries)
+//     W = (I + A)^-1, A_ij = D_ij beta_j k_i.k_j (j < i)  -> 3 terms        (the warp of the keys)
+// k, q: TI tiles of bf16 terms; g, beta: lane's token, 0 behind the end. The warps exchange the keys'
+// lengths and are otherwise on their own.
+// The sums G are exact in 64-bit fixed point (steps of 2^-32) and kept as two floats (the first a multiple
+// of 2^-10), so that differences of large sums keep their low bits.
+// W in blocks of 16: the diagonal ones by forward substitution in fp32, a half-warp per block and a
+// column per lane (as soon as t_j is known it is taken from all later rows, so that one product and one
+// selection lie between t_j and t_j+1), the one below them as -W_11 (A_10 W_00) on the tensor cores.
+// Substitution over all 32 rows took 496 products in a row of straight-line code, and the
+// warps of both kinds then waited for instructions: code size is what this routine is written for, and
+// why its loop over the depth stays a loop.
 template <int NN, int TI, int TP>
 __device__ __forceinline__ void prepare_chunk(uint32_t k, uint32_t q, uint32_t w_out, uint32_t p_out, Scalars *sc, PrepScratch *ps,
-                                              const DeltaArgs &p, float g, float beta, int chunk, int tid, int bar) {
+                                              const DeltaArgs &p, float g, float beta, bool queries, int bar) {
     constexpr int NB = NN * 2, TB = C * NB;
-    const int warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tc = lane & 3;
-    // products: warps 0, 1 keys by keys, warps 2, 3 queries by keys; each the tiles (m 0, n h), (m 1, n h), (m 1, n 2 + h)
-    const int h = warp & 1;
-    const uint32_t left = warp < 2 ? k : q;
-    float acc[3][4] = {};
-#pragma unroll
+    const int lane = threadIdx.x & 31, gr = lane >> 2, tc = lane & 3;
+    const uint32_t left = queries ? q : k;
+    // products with the keys, tiles (m, n): (0, 0), (0, 1), (1, 0), (1, 1), (1, 2), (1, 3)
+    float acc[6][4] = {};
+    float len[4] = {};
+#pragma unroll 1
     for (int ks = 0; ks < NN / 16; ++ks) {
-        uint32_t a0[TI][4], a1[TI][4], b[TI][4];
+        uint32_t a0[TI][4], a1[TI][4], b0[TI][4], b1[TI][4];
 #pragma unroll
         for (int i = 0; i < TI; ++i) {
             ldsm4(a0[i], addr_a<NB>(left + i * TB, 0, ks));
             ldsm4(a1[i], addr_a<NB>(left + i * TB, 16, ks));
-            // rows 8 h .. + 7 and 16 + 8 h .. + 7
-            ldsm4(b[i], k + i * TB + tile<NB>(8 * h + (lane & 7) + ((lane >> 4) << 4), 2 * ks + ((lane >> 3) & 1)));
+            ldsm4(b0[i], addr_b<NB>(k + i * TB, 0, ks));
+            ldsm4(b1[i], addr_b<NB>(k + i * TB, 16, ks));
         }
 #pragma unroll
         for (int x = TI - 1; x >= 0; --x)
 #pragma unroll
             for (int y = TI - 1 - x; y >= 0; --y) {
-                mma(acc[0], a0[x], b[y][0], b[y][1]);
-                mma(acc[1], a1[x], b[y][0], b[y][1]);
-                mma(acc[2], a1[x], b[y][2], b[y][3]);
+                mma(acc[0], a0[x], b0[y][0], b0[y][1]);
+                mma(acc[1], a0[x], b0[y][2], b0[y][3]);
+                mma(acc[2], a1[x], b0[y][0], b0[y][1]);
+                mma(acc[3], a1[x], b0[y][2], b0[y][3]);
+                mma(acc[4], a1[x], b1[y][0], b1[y][1]);
+                mma(acc[5], a1[x], b1[y][2], b1[y][3]);
             }
-    }
-    {   // lengths: two threads per row, keys then queries
-        const int row = (tid >> 1) & 31, half = tid & 1;
-        const uint32_t base = tid < 64 ? k : q;
-        float s = 0.f;
-        if (p.qk_norm) {
+        // the rows' squares from the same fragments: rows gr, gr + 8, 16 + gr, 24 + gr
 #pragma unroll
-            for (int c = 0; c < NN / 16; ++c) {
-                float x[8] = {};
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float x = 0.f, y = 0.f;
 #pragma unroll
                 for (int i = TI - 1; i >= 0; --i) {
-                    uint32_t u[4];
-                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
-                                 : "r"(base + i * TB + tile<NB>(row, half * (NN / 16) + c)));
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[2 * e] += lo_f(u[e]);
-                        x[2 * e + 1] += hi_f(u[e]);
-                    }
+                    const uint32_t u = (r < 2 ? a0[i] : a1[i])[(r & 1) + 2 * c];
+                    x += lo_f(u);
+                    y += hi_f(u);
                 }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s = fmaf(x[e], x[e], s);
+                len[r] = fmaf(x, x, fmaf(y, y, len[r]));
             }
-            s += __shfl_xor_sync(0xffffffffu, s, 1);
-        }
-        const float r = p.qk_norm ? rsqrtf(s + p.norm_eps) : 1.f;
-        if (half == 0) (tid < 64 ? ps->rk : ps->rq)[row] = tid < 64 ? r : r * p.scale;
     }
-    if (warp == 3) {
-        double G = g;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double x = __shfl_up_sync(0xffffffffu, G, o);
-            if (lane >= o) G += x;
-        }
-        const double last = __shfl_sync(0xffffffffu, G, 31);
-        const float hi = float(rint(G * 1024.) * (1. / 1024.));
-        ps->ghi[lane] = hi;
-        ps->glo[lane] = float(G - double(hi));
-        sc->beta[lane] = beta;
-        sc->kin[lane] = expf(float(G));
-        sc->kout[lane] = expf(float(last - G));
-        if (lane == 31) sc->whole = expf(float(last));
+    for (int r = 0; r < 4; ++r) {
+        len[r] += __shfl_xor_sync(0xffffffffu, len[r], 1);
+        len[r] += __shfl_xor_sync(0xffffffffu, len[r], 2);
     }
-    bar_sync(bar, kPrep);
-    if (warp == 0) {
-        const float in = sc->kin[lane], out = sc->kout[lane] * ps->rk[lane];
-        sc->kin[lane] = in * ps->rk[lane];
+    if (!queries) {
+        const bool fine = len[0] + len[1] + len[2] + len[3] < INFINITY && g <= 80.f && fabsf(beta) < INFINITY;
+        const bool odd = __any_sync(0xffffffffu, !fine);
+        if (lane == 0) sc->odd = odd;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) len[r] = (p.qk_norm ? rsqrtf(len[r] + p.norm_eps) : 1.f) * (queries ? p.scale : 1.f);
+    if (tc == 0) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) (queries ? ps->rq : ps->rk)[gr + 8 * r] = len[r];
+    }
+    // running sums of the log decays
+    const unsigned nan = __ballot_sync(0xffffffffu, g != g);
+    long long G = llrintf(fminf(g, 120.f) * 4294967296.f);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, G, o);
+        if (lane >= o) G += x;
+    }
+    const float bad = __int_as_float(0x7fffffff);
+    const bool seen = (nan & (0xffffffffu >> (31 - lane))) != 0;          // a NaN at or before this token
+    const float ghi = seen ? bad : float(int(G >> 22)) * 9.765625e-4f;
+    const float glo = float(int(G & 0x3fffff)) * 2.3283064365386963e-10f;
+    bar_sync(bar, kGroup);
+    const float rk = ps->rk[lane], kb = rk * beta;
+    if (queries) {
+        const long long rest = __shfl_sync(0xffffffffu, G, 31) - G;
+        const float in = seen ? bad : expf(float(G) * 2.3283064365386963e-10f);
+        const float out = (nan ? bad : expf(float(rest) * 2.3283064365386963e-10f)) * rk;
+        sc->kin[lane] = in * rk;
         sc->qin[lane] = in * ps->rq[lane];
         sc->kout[lane] = out;
-        sc->out[lane] = out * sc->beta[lane];
+        sc->out[lane] = out * beta;
+        sc->beta[lane] = beta;
+        if (lane == 31) sc->whole = nan ? bad : in;
     }
+    {   // D and the factors of rows and columns: rows gr + 8 i, columns 8 n + 2 tc, + 1
+        float rh[4], rl[4], ch[8], cl[8], cb[8];
 #pragma unroll
-    for (int x = 0; x < 3; ++x) {
-        const int m = x ? 16 : 0, n0 = (x == 2 ? 16 : 0) + 8 * h;
+        for (int i = 0; i < 4; ++i) {
+            rh[i] = __shfl_sync(0xffffffffu, ghi, gr + 8 * i);
+            rl[i] = __shfl_sync(0xffffffffu, glo, gr + 8 * i);
+        }
 #pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-            const int i = m + gr + 4 * e;                   // e = 0: row gr, e = 2: row gr + 8
-            float v[2];
+        for (int j = 0; j < 8; ++j) {
+            const int from = 8 * (j >> 1) + 2 * tc + (j & 1);
+            ch[j] = __shfl_sync(0xffffffffu, ghi, from);
+            cl[j] = __shfl_sync(0xffffffffu, glo, from);
+            cb[j] = __shfl_sync(0xffffffffu, kb, from);
+        }
+        const int last = queries ? 0 : -1;      // column j of row i stays if j <= i + last
 #pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                const int j = n0 + 2 * tc + f;
-                const float d = expf((ps->ghi[i] - ps->ghi[j]) + (ps->glo[i] - ps->glo[j]));
-                const float s = acc[x][e + f] * d * (ps->rk[j] * sc->beta[j]);
-                v[f] = warp < 2 ? (j < i ? s * ps->rk[i] : 0.f) : (j <= i ? s * ps->rq[i] : 0.f);
+        for (int x = 0; x < 6; ++x) {
+            const int m = x < 2 ? 0 : 1, n = x < 2 ? x : x - 2;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int ri = 2 * m + (e >> 1), ci = 2 * n + (e & 1);
+                const float w = acc[x][e] * fast_exp((rh[ri] - ch[ci]) + (rl[ri] - cl[ci])) * (cb[ci] * len[ri]);
+                acc[x][e] = 8 * n + 2 * tc + (e & 1) <= gr + 8 * ri + last ? w : 0.f;
             }
-            const int j = n0 + 2 * tc;
-            if (warp < 2) {
-                *reinterpret_cast<float2 *>(&ps->A[i * kAs + j]) = make_float2(v[0], v[1]);
-            } else {
+        }
+    }
+    if (queries) {
+#pragma unroll
+        for (int x = 0; x < 6; ++x) {
+            const int m = x < 2 ? 0 : 1, n = x < 2 ? x : x - 2;
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
                 uint32_t r[TP];
-                split2<TP>(v[0], v[1], r);
+                split2<TP>(acc[x][e], acc[x][e + 1], r);
 #pragma unroll
-                for (int k2 = 0; k2 < TP; ++k2)
-                    asm volatile("st.shared.b32 [%0], %1;" :: "r"(p_out + k2 * kTri + x * 512 + block(i & 15, (j >> 3) & 1) + ((j & 7) << 1)), "r"(r[k2]) : "memory");
+                for (int z = 0; z < TP; ++z) st_b32(p_out + z * kTri + (m + (n >> 1)) * 512 + block(gr + 4 * e, n & 1) + 4 * tc, r[z]);
             }
         }
+        return;
     }
-    bar_sync(bar, kPrep);
-    if (warp == (chunk & 3)) {
-        float t[C];
+    // the diagonal blocks, by columns
 #pragma unroll
-        for (int i = 0; i < C; ++i) {
-            float s[4] = {};
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int kk = 0; kk < i; kk += 4) {
-                const float4 a = *reinterpret_cast<const float4 *>(&ps->A[i * kAs + kk]);
-                s[0] = fmaf(a.x, t[kk], s[0]);
-                if (kk + 1 < i) s[1] = fmaf(a.y, t[kk + 1], s[1]);
-                if (kk + 2 < i) s[2] = fmaf(a.z, t[kk + 2], s[2]);
-                if (kk + 3 < i) s[3] = fmaf(a.w, t[kk + 3], s[3]);
-            }
-            t[i] = i < lane ? 0.f : (i == lane ? 1.f : -((s[0] + s[1]) + (s[2] + s[3])));
-            ps->T[i * kAs + lane] = t[i];
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ps->A[b][(8 * n + 2 * tc + (e & 1)) * kAs + gr + 8 * (e >> 1)] = acc[4 * b + n][e];
+    __syncwarp();
+    const int col = lane & 15;
+    float *D = ps->A[lane >> 4];
+    float t[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t[i] = i == col ? 1.f : 0.f;
+#pragma unroll
+    for (int j = 0; j < 15; ++j) {
+        t[j] = j < col ? 0.f : t[j];
+#pragma unroll
+        for (int i = (j + 1) >> 2; i < 4; ++i) {
+            const float4 a = *reinterpret_cast<const float4 *>(&D[j * kAs + 4 * i]);
+            const float v[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (4 * i + e > j) t[4 * i + e] = fmaf(-v[e], t[j], t[4 * i + e]);
         }
     }
-    bar_sync(bar, kPrep);
+    t[15] = 15 < col ? 0.f : t[15];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) D[i * kAs + col] = t[i];
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {   // row `col` of this half-warp's block
+        const float4 x = *reinterpret_cast<const float4 *>(&D[col * kAs + 8 * c]), y = *reinterpret_cast<const float4 *>(&D[col * kAs + 8 * c + 4]);
+        uint32_t w[4][3];
+        split2<3>(x.x, x.y, w[0]);
+        split2<3>(x.z, x.w, w[1]);
+        split2<3>(y.x, y.y, w[2]);
+        split2<3>(y.z, y.w, w[3]);
+#pragma unroll
+        for (int z = 0; z < 3; ++z)
+            st_v4(w_out + z * kTri + (lane >> 4) * 1024 + block(col, c), w[0][z], w[1][z], w[2][z], w[3][z]);
+    }
+    __syncwarp();
+    // the block below: -W_11 (A_10 W_00)
+    float v[2][4] = {}, r[2][4] = {};
     {
-        const int i = tid >> 2, c = tid & 3;                // row, eight columns 8 c ..
-        if (i >= 16 || c < 2) {
-            const float4 x = *reinterpret_cast<const float4 *>(&ps->T[i * kAs + 8 * c]);
-            const float4 y = *reinterpret_cast<const float4 *>(&ps->T[i * kAs + 8 * c + 4]);
-            uint32_t w[4][3];
-            split2<3>(x.x, x.y, w[0]);
-            split2<3>(x.z, x.w, w[1]);
-            split2<3>(y.x, y.y, w[2]);
-            split2<3>(y.z, y.w, w[3]);
-            const int bl = (i >> 4) + (c >> 1);             // 0, 1 or 2
+        uint32_t a[3][4], w[3][4];
+        split_a<3>(acc[2], acc[3], a);
 #pragma unroll
-            for (int k2 = 0; k2 < 3; ++k2)
-                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(w_out + k2 * kTri + bl * 512 + block(i & 15, c & 1)),
-                             "r"(w[0][k2]), "r"(w[1][k2]), "r"(w[2][k2]), "r"(w[3][k2]) : "memory");
-        }
+        for (int z = 0; z < 3; ++z) ldsm4t(w[z], addr_block_t(w_out + z * kTri));
+#pragma unroll
+        for (int x = 2; x >= 0; --x)
+#pragma unroll
+            for (int z = 2 - x; z >= 0; --z) {
+                mma(v[0], a[x], w[z][0], w[z][1]);
+                mma(v[1], a[x], w[z][2], w[z][3]);
+            }
     }
+    // A row that is not finite would reach the rows above it through the zeros of W_11; it needs no
+    // place here, since its own token is already marked where the values are.
+    auto put = [&](const float (&x)[2][4], bool neg) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                uint32_t u[3];
+                split2<3>(neg ? -x[n][e] : x[n][e], neg ? -x[n][e + 1] : x[n][e + 1], u);
+#pragma unroll
+                for (int z = 0; z < 3; ++z) st_b32(w_out + z * kTri + 512 + block(gr + 4 * e, n) + 4 * tc, u[z]);
+            }
+    };
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[n][e] = fabsf(v[n][e]) < INFINITY ? v[n][e] : 0.f;
+    put(v, false);
+    __syncwarp();
+    {
+        uint32_t a[3][4], w[3][4];
+#pragma unroll
+        for (int z = 0; z < 3; ++z) {
+            ldsm4(a[z], addr_block_t(w_out + z * kTri + 1024));     // by rows, as a left operand
+            ldsm4t(w[z], addr_block_t(w_out + z * kTri + 512));
+        }
+#pragma unroll
+        for (int x = 2; x >= 0; --x)
+#pragma unroll
+            for (int z = 2 - x; z >= 0; --z) {
+                mma(r[0], a[x], w[z][0], w[z][1]);
+                mma(r[1], a[x], w[z][2], w[z][3]);
+            }
+    }
+    __syncwarp();
+    put(r, true);
 }
 
 }  // namespace dm
