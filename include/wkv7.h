@@ -458,6 +458,29 @@ WKV7_API wkv7_status wkv7_delta_forward(int B, int T, int H, int Hk, int N, wkv7
                                         const wkv7_delta_opts *opts, void *stream);
 
 /*
+ * Backward of wkv7_delta_forward: the gradients of L = <dy, y> + <dS_T, S_T> with respect to every
+ * input, the chain rule through the three lines above (through the lengths of q and k with qk_norm; q's
+ * includes scale). q, k, v, g, beta, S0 and opts are the forward's; dy [rows][H][N] of dt, dense;
+ * dS_T [B][H][N][N] fp32 or NULL (zero). Outputs, dense and of dt: dq, dk [rows][Hk][N] (summed over
+ * the value heads of a key head, in a fixed order), dv [rows][H][N], dg, dbeta [rows][H]; dS0
+ * [B][H][N][N] fp32 or NULL, may equal dS_T (in place). Rows behind the last packed sequence are not
+ * written. A log decay of -inf has gradient 0. Repeated calls give identical results.
+ * Workspace: wkv7_delta_backward_workspace_bytes(...) bytes, no initial contents, not shared by calls
+ * that may overlap in time. Errors as wkv7_delta_forward, plus WKV7_ERR_WORKSPACE.
+ */
+WKV7_API wkv7_status wkv7_delta_backward(int B, int T, int H, int Hk, int N, wkv7_dtype dt,
+                                         const void *q, const void *k, const void *v, const void *g,
+                                         const void *beta, const float *S0, const void *dy,
+                                         const float *dS_T, void *dq, void *dk, void *dv, void *dg,
+                                         void *dbeta, float *dS0, const wkv7_delta_opts *opts,
+                                         void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of wkv7_delta_backward (opts: only whether cu_seqlens is set matters; NULL =
+ * defaults). 0 without rows or for invalid arguments. Host only. */
+WKV7_API size_t wkv7_delta_backward_workspace_bytes(int B, int T, int H, int Hk, int N, wkv7_dtype dt,
+                                                    const wkv7_delta_opts *opts);
+
+/*
  * One token for each of B rows against a pool of n_slots states: row b advances S[slots[b]] in
  * place. q, k [B][Hk][N], v, y [B][H][N], g, beta [B][H] of dt; S [n_slots][H][N][N] fp32; slots
  * device int32 [B], or NULL (row b takes slot b; n_slots must then be at least B). A row whose slot

@@ -901,6 +901,65 @@ wkv7_status wkv7_delta_forward(int B, int T, int H, int Hk, int N, wkv7_dtype dt
     return e == cudaSuccess ? WKV7_OK : cuda_fail(e, "gated-delta forward launch");
 }
 
+size_t wkv7_delta_backward_workspace_bytes(int B, int T, int H, int Hk, int N, wkv7_dtype dt, const wkv7_delta_opts *opts_in) {
+    wkv7_delta_opts o;
+    size_t rows = 0;
+    if (delta_args(B, T, H, Hk, N, dt, opts_in, o, rows) != WKV7_OK || rows == 0) return 0;
+    return wkv7::delta_backward_workspace(rows, B, H, N, dt);
+}
+
+wkv7_status wkv7_delta_backward(int B, int T, int H, int Hk, int N, wkv7_dtype dt, const void *q, const void *k,
+                                const void *v, const void *g, const void *beta, const float *S0, const void *dy,
+                                const float *dS_T, void *dq, void *dk, void *dv, void *dg, void *dbeta, float *dS0,
+                                const wkv7_delta_opts *opts_in, void *workspace, size_t workspace_bytes, void *stream) {
+    g_err[0] = '\0';
+    wkv7_delta_opts o;
+    size_t rows = 0;
+    wkv7_status st = delta_args(B, T, H, Hk, N, dt, opts_in, o, rows);
+    if (st != WKV7_OK) return st;
+    if ((rows / 64 + B) * static_cast<size_t>(Hk) > size_t(INT_MAX)) return fail(WKV7_ERR_ARG, "sizes overflow");
+    const size_t need = rows ? wkv7::delta_backward_workspace(rows, B, H, N, dt) : 0;
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(WKV7_ERR_WORKSPACE, "workspace of %zu bytes required, %zu given", need, workspace ? workspace_bytes : 0);
+    const size_t kw = size_t(Hk) * N, vw = size_t(H) * N, el = elem_bytes(dt), gb = rows * H * el;
+    const size_t sb = size_t(B) * H * N * N * 4;
+    // inputs 0-8, outputs 9-14, workspace 15
+    const Buf bufs[] = {{"q", q, strided_bytes(rows, kw, o.q_stride, dt)},
+                        {"k", k, strided_bytes(rows, kw, o.k_stride, dt)},
+                        {"v", v, strided_bytes(rows, vw, o.v_stride, dt)},
+                        {"g", g, gb},
+                        {"beta", beta, gb},
+                        {"cu_seqlens", o.cu_seqlens, o.cu_seqlens ? size_t(B + 1) * 4 : 0},
+                        {"S0", S0, S0 ? sb : 0},
+                        {"dy", dy, rows * vw * el},
+                        {"dS_T", dS_T, dS_T ? sb : 0},
+                        {"dq", dq, rows * kw * el},
+                        {"dk", dk, rows * kw * el},
+                        {"dv", dv, rows * vw * el},
+                        {"dg", dg, gb},
+                        {"dbeta", dbeta, gb},
+                        {"dS0", dS0, dS0 ? sb : 0},
+                        {"workspace", workspace, need}};
+    st = check_buffers(bufs, 16, 9, [&](int x, int i) { return x == 14 && i == 8 && dS0 == dS_T; });
+    if (st != WKV7_OK) return st;
+    wkv7::DeltaArgs p = delta_launch(B, T, H, Hk, N, dt, q, k, v, g, beta, nullptr, o, stream);
+    p.S0 = S0;
+    p.dy = dy;
+    p.dS_T = dS_T;
+    p.dq = dq; p.dk = dk; p.dv = dv; p.dg = dg; p.dbeta = dbeta;
+    p.dS0 = dS0;
+    p.keep_E = workspace;
+    if (rows == 0) {                // dS0 <- dS_T (or zeros)
+        if (!dS0 || dS0 == dS_T) return WKV7_OK;
+        wkv7::FwdArgs c{};
+        c.B = B; c.H = H; c.N = N; c.S0 = dS_T; c.S_T = dS0; c.stream = p.stream;
+        const cudaError_t e = wkv7::launch_copy_state(c);
+        return e == cudaSuccess ? WKV7_OK : cuda_fail(e, "state-gradient copy launch");
+    }
+    const cudaError_t e = wkv7::launch_delta_backward(p);
+    return e == cudaSuccess ? WKV7_OK : cuda_fail(e, "gated-delta backward launch");
+}
+
 wkv7_status wkv7_delta_step(int B, int H, int Hk, int N, wkv7_dtype dt, const void *q, const void *k, const void *v,
                             const void *g, const void *beta, float *S, int n_slots, const int *slots, void *y,
                             const wkv7_delta_opts *opts_in, void *stream) {

@@ -26,11 +26,28 @@ struct DeltaArgs {
     float *S;
     int n_slots;
     const int *slots;       // nullable: row b takes slot b
+    // backward
+    const void *dy;
+    const float *dS_T;      // nullable
+    void *dq, *dk, *dv, *dg, *dbeta;
+    float *dS0;             // nullable
+    void *keep_E;           // workspace: the errors, [rows][H][N] (bf16: two terms, keep_lo elements apart)
+    long long keep_lo;
+    void *keep_dlo;         // workspace, bf16: the second term of dv
+    void *keep_S, *keep_dS; // workspace: the state a chunk of 64 tokens starts from and its last state's gradient
+    long long keep_second;  // bf16: elements from their first terms to the second
     cudaStream_t stream;
 };
 
 cudaError_t launch_delta_forward(const DeltaArgs &p);
 cudaError_t launch_delta_step(const DeltaArgs &p);
+cudaError_t launch_delta_states(const DeltaArgs &p);        // keep_E, keep_S
+cudaError_t launch_delta_backward(const DeltaArgs &p);      // the three kernels of the backward
+size_t delta_backward_workspace(size_t rows, int B, int H, int N, wkv7_dtype dt);
+
+// Chunks of 64 tokens are numbered over all sequences so that each has a place of its own without a pass over
+// the lengths: sequence s starts at number (first row) / 64 + s, and there are at most rows / 64 + B.
+__host__ __device__ __forceinline__ long long delta_slot(long long first_row, int s) { return first_row / 64 + s; }
 
 // Rows [first, last) of sequence s. Packed bounds outside 0..T or decreasing are clamped, so that no
 // row outside the buffers is reached.

@@ -1,0 +1,783 @@
+// The gated delta rule's backward, in three kernels. With the chunk quantities of delta_chunk.cu and
+// dS' the gradient of a chunk's last state:
+//   1. delta_chunk_kernel with STATES (delta_chunk.cu): the errors E, and the state every 64 tokens start from.
+//   2. delta_reverse_kernel: the chain back through the chunks of 32,
+//          dE = P^T dY + out (K dS'^T),   dX = W^T dE,   dV = dX,
+//          dS = exp(G_C) dS' + (qin dY)^T Q - (kin dX)^T K
+//      (out, qin, kin: the scalars of delta_mma.cuh). As forward, the rows of dS never meet: a warp owns 16 of
+//      them, in accumulators, and the chain runs through its registers.
+//   3. delta_grad_kernel: everything that contracts over the value channels, for all chunks of 64 at once:
+//          A = dY E^T (j <= i), B = dX E^T (j < i), n = sq_i rk_j D beta_j A, o = rk_i rk_j D beta_j B
+//          sq dQ = n K + qin (dY S),    rk dK = n^T Q - o K - o^T K + out (E dS') - kin (dX S)
+//          z = (n (Q K^T) - o (K K^T)) / beta_j,   tail_j = kout_j k_j.(E dS')_j
+//          dbeta_j = sum_i z_ij + tail_j
+//          dG_i = sum_j beta_j z_ij + q_i.(qin dY S)_i - k_i.(kin dX S)_i - beta_i dbeta_i
+//          dg_t = sum_{i >= t} dG_i + sum_j beta_j tail_j + exp(G_C) <S, dS'>
+//      (rk, sq: 1 / |k| and scale / |q|; with unit keys dk = rk dK - k^ (k^.rk dK), and q alike).
+//      The value heads of one key head are summed in the same accumulators, in order.
+// Precision: the chain of dS keeps three bf16 terms wherever a state or its gradient is read or written. For
+// outputs in bf16, everything computed (E, dX, S, dS', n, o) enters the sums in two terms, 16 bits: dg is a
+// difference of large sums and would show a single term's rounding several times over.
+#include "delta_mma.cuh"
+
+namespace wkv7 {
+
+using namespace dm;
+
+namespace {
+
+template <int NN, int RW, bool F32>
+struct RevLayout {
+    static constexpr int TI = F32 ? 3 : 1, TP = 3;
+    static constexpr int KB = TI * C * NN * 2, YB = TI * C * RW * 32;
+    static constexpr int kK = 0, kQ = KB, kY = 2 * KB, kW = kY + YB, kP = kW + 3 * kTri, kS = kP + TP * kTri;
+    static constexpr int stage = (kS + int(sizeof(Scalars)) + 127) / 128 * 128;
+    static constexpr int stages = F32 ? (NN == 64 ? 4 : 3) : (NN == 64 ? 5 : 6);
+    static constexpr int total = stages * stage + kGroups * int(sizeof(PrepScratch));
+    static constexpr int threads = RW * 32 + kGroups * kGroup, meet = RW * 32 + kGroup;
+};
+
+template <int NN, int RW, bool F32>
+__global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64) ? 2 : 1) delta_reverse_kernel(const DeltaArgs p) {
+    using L = RevLayout<NN, RW, F32>;
+    using Tin = std::conditional_t<F32, float, __nv_bfloat16>;
+    constexpr int TI = L::TI, NB = NN * 2, TB = C * NB, YNB = RW * 32, YTB = C * YNB;
+    extern __shared__ __align__(128) unsigned char sm[];
+    const uint32_t base = smem_addr(sm);
+    constexpr int slices = NN / (16 * RW);
+    const unsigned unit = blockIdx.x / slices;
+    const int row0 = (blockIdx.x % slices) * 16 * RW;
+    const int s = unit / unsigned(p.H), h = unit % unsigned(p.H), hk = h / (p.H / p.Hk);
+    long long t0, t1;
+    delta_rows(p.cu, p.T, s, t0, t1);
+    const int chunks = int((t1 - t0 + C - 1) / C);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int full = 1 + kGroups, empty = full + L::stages;
+
+    // step r takes chunk chunks - 1 - r
+    if (warp >= RW) {
+        const int group = (warp - RW) >> 1, tid = (threadIdx.x - RW * 32) % kGroup;
+        PrepScratch *ps = reinterpret_cast<PrepScratch *>(sm + L::stages * L::stage) + group;
+        const long long first = t0 + (long long)(chunks - 1 - group) * C;
+        RowLoader<NN, F32> k(p.k, first, (long long)hk * NN, p.ks, tid), q(p.q, first, (long long)hk * NN, p.qs, tid);
+        RowLoader<RW * 16, F32> dy(p.dy, first, (long long)h * NN + row0, (long long)p.H * NN, tid);
+        Gate<F32> gate, next{};
+        auto load = [&](int r) {
+            const uint32_t st = base + (r % L::stages) * L::stage;
+            const long long at = (long long)(chunks - 1 - r) * C;
+            const int n = int(min((long long)C, t1 - t0 - at));
+            next.load(p.g, p.beta, (t0 + at + lane) * p.H + h, lane < n);
+            k.load(st + L::kK, n);
+            q.load(st + L::kQ, n);
+            dy.load(st + L::kY, n);
+            k.advance(-kGroups);
+            q.advance(-kGroups);
+            dy.advance(-kGroups);
+            cp_commit();
+        };
+        if (group < chunks) load(group);
+        for (int r = group; r < chunks; r += kGroups) {
+            gate = next;
+            if (r + kGroups < chunks) {
+                if (r + kGroups >= L::stages) bar_sync(empty + (r + kGroups) % L::stages, L::meet);
+                load(r + kGroups);
+                cp_wait<1>();
+            } else {
+                cp_wait<0>();
+            }
+            bar_sync(1 + group, kGroup);
+            unsigned char *st = sm + (r % L::stages) * L::stage;
+            const uint32_t sa = base + (r % L::stages) * L::stage;
+            const bool queries = ((warp ^ (r / kGroups)) & 1) != 0;
+            prepare_chunk<NN, TI, 3>(sa + L::kK, sa + L::kQ, st + L::kW, sa + L::kP, reinterpret_cast<Scalars *>(st + L::kS), ps, p,
+                                     delta_clamp(gate.num(gate.g)), gate.num(gate.beta), queries, 1 + group);
+            bar_arrive(full + r % L::stages, L::meet);
+        }
+        return;
+    }
+
+    const int gr = lane >> 2, tc = lane & 3, row = row0 + 16 * warp;
+    const size_t so = (size_t(unit) * NN + row) * NN;
+    float S[NN / 8][4];             // dS
+#pragma unroll
+    for (int n = 0; n < NN / 8; ++n) {
+        float2 a = make_float2(0, 0), b = a;
+        if (p.dS_T) {
+            a = *reinterpret_cast<const float2 *>(p.dS_T + so + gr * NN + 8 * n + 2 * tc);
+            b = *reinterpret_cast<const float2 *>(p.dS_T + so + (gr + 8) * NN + 8 * n + 2 * tc);
+        }
+        S[n][0] = a.x; S[n][1] = a.y; S[n][2] = b.x; S[n][3] = b.y;
+    }
+    Tin *dv = static_cast<Tin *>(p.dv) + size_t(h) * NN + row;
+    [[maybe_unused]] Tin *dlo = static_cast<Tin *>(p.keep_dlo) + size_t(h) * NN + row;
+    const size_t ys = size_t(p.H) * NN;
+    const long long slot0 = delta_slot(t0, s);
+    const int tok_l = (lane & 7) + ((lane >> 4) << 3), col_l = 2 * warp + ((lane >> 3) & 1);
+    for (int r = 0; r < chunks; ++r) {
+        const int c = chunks - 1 - r;
+        const uint32_t st = base + (r % L::stages) * L::stage;
+        const Scalars *sc = reinterpret_cast<const Scalars *>(sm + (r % L::stages) * L::stage + L::kS);
+        const long long t = t0 + (long long)c * C;
+        const int n_tok = int(min((long long)C, t1 - t));
+        if (r == 0 || c % 2 == 1) keep_state<F32, NN>(p.keep_dS, p.keep_second, (slot0 + c / 2) * p.H + h, row, S);
+        bar_sync(full + r % L::stages, L::meet);
+        // dE^T = out (dS K^T) + dY^T P
+        float E[4][4] = {};
+#pragma unroll
+        for (int ks = 0; ks < NN / 16; ++ks) {
+            uint32_t a[3][4], b[TI][2][4];
+            split_a<3>(S[2 * ks], S[2 * ks + 1], a);
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) ldsm4(b[i][n], addr_b<NB>(st + L::kK + i * TB, 16 * n, ks));
+#pragma unroll
+            for (int x = 2; x >= 0; --x)
+#pragma unroll
+                for (int z = TI - 1; z >= 0; --z) {
+                    if (x + z > 2) continue;
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) mma(E[n], a[x], b[z][n >> 1][2 * (n & 1)], b[z][n >> 1][2 * (n & 1) + 1]);
+                }
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const float2 o = *reinterpret_cast<const float2 *>(&sc->out[8 * n + 2 * tc]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) E[n][e] *= e & 1 ? o.y : o.x;
+        }
+        uint32_t y[2][TI][4];       // dY^T: rows are value channels, depth tokens
+#pragma unroll
+        for (int ib = 0; ib < 2; ++ib) {
+#pragma unroll
+            for (int i = 0; i < TI; ++i) ldsm4t(y[ib][i], st + L::kY + i * YTB + tile<YNB>(16 * ib + tok_l, col_l));
+#pragma unroll
+            for (int jb = 0; jb <= ib; ++jb) {
+                uint32_t w[3][4];
+#pragma unroll
+                for (int z = 0; z < 3; ++z) ldsm4t(w[z], addr_block_t(st + L::kP + z * kTri + (ib + jb) * 512));
+#pragma unroll
+                for (int x = TI - 1; x >= 0; --x)
+#pragma unroll
+                    for (int z = 2 - x; z >= 0; --z) {
+                        mma(E[2 * jb], y[ib][x], w[z][0], w[z][1]);
+                        mma(E[2 * jb + 1], y[ib][x], w[z][2], w[z][3]);
+                    }
+            }
+        }
+        // dX^T = dE^T W
+        float X[4][4] = {};
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            uint32_t a[3][4];
+            split_a<3>(E[2 * kb], E[2 * kb + 1], a);
+#pragma unroll
+            for (int jb = 0; jb <= kb; ++jb) {
+                uint32_t w[3][4];
+#pragma unroll
+                for (int z = 0; z < 3; ++z) ldsm4t(w[z], addr_block_t(st + L::kW + z * kTri + (kb + jb) * 512));
+#pragma unroll
+                for (int x = 2; x >= 0; --x)
+#pragma unroll
+                    for (int z = 2 - x; z >= 0; --z) {
+                        mma(X[2 * jb], a[x], w[z][0], w[z][1]);
+                        mma(X[2 * jb + 1], a[x], w[z][2], w[z][3]);
+                    }
+            }
+        }
+        // dS <- exp(G_C) dS + (qin dY)^T Q - (kin dX)^T K
+        const float whole = sc->whole;
+#pragma unroll
+        for (int n = 0; n < NN / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[n][e] *= whole;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            uint32_t a[3][4], d[3][4];
+            float u[2][4], w[2][4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const float2 f = *reinterpret_cast<const float2 *>(&sc->qin[16 * kb + 8 * n + 2 * tc]);
+                const float2 z = *reinterpret_cast<const float2 *>(&sc->kin[16 * kb + 8 * n + 2 * tc]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = 0.f;
+#pragma unroll
+                    for (int i = TI - 1; i >= 0; --i) {
+                        const uint32_t v = y[kb][i][2 * n + (e >> 1)];
+                        x += e & 1 ? hi_f(v) : lo_f(v);
+                    }
+                    u[n][e] = x * (e & 1 ? f.y : f.x);
+                    w[n][e] = X[2 * kb + n][e] * -(e & 1 ? z.y : z.x);
+                }
+            }
+            split_a<3>(u[0], u[1], a);
+            split_a<3>(w[0], w[1], d);
+#pragma unroll
+            for (int n = 0; n < NN / 16; ++n) {
+                uint32_t bq[TI][4], bk[TI][4];
+#pragma unroll
+                for (int z = 0; z < TI; ++z) {
+                    ldsm4t(bq[z], addr_bt<NB>(st + L::kQ + z * TB, 16 * kb, 2 * n));
+                    ldsm4t(bk[z], addr_bt<NB>(st + L::kK + z * TB, 16 * kb, 2 * n));
+                }
+#pragma unroll
+                for (int x = 2; x >= 0; --x)
+#pragma unroll
+                    for (int z = TI - 1; z >= 0; --z) {
+                        if (x + z > 2) continue;
+                        mma(S[2 * n], a[x], bq[z][0], bq[z][1]);
+                        mma(S[2 * n + 1], a[x], bq[z][2], bq[z][3]);
+                        mma(S[2 * n], d[x], bk[z][0], bk[z][1]);
+                        mma(S[2 * n + 1], d[x], bk[z][2], bk[z][3]);
+                    }
+            }
+        }
+        if constexpr (F32) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 8 * n + 2 * tc + (e & 1);
+                    if (i < n_tok) dv[(t + i) * ys + gr + 8 * (e >> 1)] = X[n][e];
+                }
+        } else {                    // through dY's place (this warp's own columns), in two terms
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                __syncwarp();
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float *x = &X[2 * m + i][2 * e];
+                            o[2 * i + e] = pack(x[0], x[1]);
+                            x[0] -= lo_f(o[2 * i + e]);
+                            x[1] -= hi_f(o[2 * i + e]);
+                        }
+                    stsm4t(st + L::kY + tile<YNB>(16 * m + tok_l, col_l), o);
+                }
+                __syncwarp();
+                Tin *to = half ? dlo : dv;
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const int tok = 16 * m + (lane >> 1);
+                    uint4 o;
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
+                                 : "r"(st + L::kY + tile<YNB>(tok, 2 * warp + (lane & 1))) : "memory");
+                    if (tok < n_tok) *reinterpret_cast<uint4 *>(to + (t + tok) * ys + 8 * (lane & 1)) = o;
+                }
+            }
+        }
+        if (r + L::stages < chunks) bar_arrive(empty + r % L::stages, L::meet);
+    }
+    if (p.dS0) {
+#pragma unroll
+        for (int n = 0; n < NN / 8; ++n) {
+            *reinterpret_cast<float2 *>(p.dS0 + so + gr * NN + 8 * n + 2 * tc) = make_float2(S[n][0], S[n][1]);
+            *reinterpret_cast<float2 *>(p.dS0 + so + (gr + 8) * NN + 8 * n + 2 * tc) = make_float2(S[n][2], S[n][3]);
+        }
+    }
+}
+
+// ---- the gradients of a chunk of 64 tokens ------------------------------------------------------------
+
+constexpr int GC = 64, GT = 512;        // tokens, threads (16 warps: 4 row blocks of 16 by 4 column groups)
+
+template <int NN, bool F32>
+struct GradLayout {
+    static constexpr int TI = F32 ? 3 : 1, TE = F32 ? 3 : 2, DW = F32 ? 32 : 64;   // DW: value channels at a time
+    static constexpr int KB = GC * NN * 2, YB = GC * DW * 2, SB = DW * NN * 2, MB = GC * GC * 2;   // one term each
+    static constexpr int kK = 0, kQ = TI * KB, kSlice = 2 * TI * KB;
+    static constexpr int kY = kSlice, kE = kY + TI * YB, kX = kE + TE * YB, kS = kX + TE * YB, kD = kS + TE * SB;
+    static constexpr int kN = kSlice, kO = kN + TE * MB;                 // n and -o, where the slice was
+    static constexpr int slice_end = kD + TE * SB, mats_end = kO + TE * MB;
+    static constexpr int kF = slice_end > mats_end ? slice_end : mats_end;
+};
+struct GradScalars {
+    float ghi[GC], glo[GC], rk[GC], sq[GC], beta[GC], kin[GC], qin[GC], kout[GC], out[GC];
+    float row[4][GC], tail[4][GC], col[4][GC], dq[4][GC], dk[4][GC];
+    float ss[GT / 32];
+    float whole;
+};
+
+// `rows` rows of W elements (rows from n on as zeros) from an array of the inputs' type (bf16: asynchronous) into
+// tiles of bf16 terms (fp32: three, TERM bytes apart).
+template <int W, bool F32>
+__device__ __forceinline__ void load_rows(uint32_t dst, const void *src, long long stride, int rows, int n, int term) {
+    for (int i = threadIdx.x; i < rows * (W / 8); i += GT) {
+        const int r = i / (W / 8), c = i % (W / 8);
+        const uint32_t to = dst + tile<W * 2>(r, c);
+        if constexpr (!F32) {
+            const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(src);
+            cp16(to, r < n ? p + r * stride + 8 * c : p, r < n);
+        } else {
+            float4 x = make_float4(0, 0, 0, 0), y = x;
+            if (r < n) {
+                const float *p = static_cast<const float *>(src) + r * stride + 8 * c;
+                x = *reinterpret_cast<const float4 *>(p);
+                y = *reinterpret_cast<const float4 *>(p + 4);
+            }
+            uint32_t w[4][3];
+            split2<3>(x.x, x.y, w[0]);
+            split2<3>(x.z, x.w, w[1]);
+            split2<3>(y.x, y.y, w[2]);
+            split2<3>(y.z, y.w, w[3]);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) st_v4(to + k * term, w[0][k], w[1][k], w[2][k], w[3][k]);
+        }
+    }
+}
+
+// d[0 .. 2 CT) += a b over the pairs of terms that count: a TA terms of a left operand, b TB terms of
+// right operands of 16 columns each.
+template <int TA, int TB, int CT>
+__device__ __forceinline__ void mma_terms(float (&d)[CT][4], const uint32_t (&a)[TA][4], const uint32_t (&b)[TB][CT / 2][4]) {
+    constexpr int most = (TA > TB ? TA : TB) - 1;
+#pragma unroll
+    for (int x = TA - 1; x >= 0; --x)
+#pragma unroll
+        for (int z = TB - 1; z >= 0; --z) {
+            if (x + z > most) continue;
+#pragma unroll
+            for (int n = 0; n < CT; ++n) mma(d[n], a[x], b[z][n >> 1][2 * (n & 1)], b[z][n >> 1][2 * (n & 1) + 1]);
+        }
+}
+
+__device__ __forceinline__ float quad_sum(float x) {        // over the lanes of one row
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+__device__ __forceinline__ float col_sum(float x) {         // over the eight rows of a tile
+    x += __shfl_xor_sync(0xffffffffu, x, 4);
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+// Elements (r, 2 words of columns c, c + 1) of a tile of TI terms.
+template <int NB, int TI>
+__device__ __forceinline__ float2 pair_at(uint32_t base, int term, int r, int c) {
+    float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = TI - 1; i >= 0; --i) {
+        uint32_t u;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(u) : "r"(base + i * term + tile<NB>(r, c >> 3) + ((c & 7) << 1)));
+        v.x += lo_f(u);
+        v.y += hi_f(u);
+    }
+    return v;
+}
+
+template <int NN, bool F32>
+__global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p) {
+    using L = GradLayout<NN, F32>;
+    using Tin = std::conditional_t<F32, float, __nv_bfloat16>;
+    constexpr int TI = L::TI, TE = L::TE, DW = L::DW, NB = NN * 2, YNB = DW * 2, CT = NN / 32, CW = NN / 4;
+    extern __shared__ __align__(128) unsigned char sm[];
+    const uint32_t base = smem_addr(sm);
+    GradScalars *sc = reinterpret_cast<GradScalars *>(sm + L::kF);
+    const int hk = blockIdx.x % unsigned(p.Hk);
+    const long long slot = blockIdx.x / unsigned(p.Hk);
+    // the sequence of this chunk: the last one that starts at or before it
+    int s = 0;
+    for (int lo = 0, hi = p.B; lo < hi;) {
+        const int mid = (lo + hi) >> 1;
+        const long long first = p.cu ? min(max(p.cu[mid], 0), p.T) : (long long)mid * p.T;
+        if (delta_slot(first, mid) <= slot) {
+            s = mid;
+            lo = mid + 1;
+        } else {
+            hi = mid;
+        }
+    }
+    long long t0, t1;
+    delta_rows(p.cu, p.T, s, t0, t1);
+    const long long chunk = slot - delta_slot(t0, s);
+    t0 += chunk * GC;
+    if (chunk < 0 || t0 >= t1) return;
+    const int n = int(min((long long)GC, t1 - t0));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tc = lane & 3;
+    const int wr = warp & 3, wc = warp >> 2, c0 = wc * CW, j0 = wc * 16;   // rows 16 wr; key channels c0; tokens j0 ..
+    const int group = p.H / p.Hk;
+
+    load_rows<NN, F32>(base + L::kK, static_cast<const Tin *>(p.k) + t0 * p.ks + hk * NN, p.ks, GC, n, L::KB);
+    load_rows<NN, F32>(base + L::kQ, static_cast<const Tin *>(p.q) + t0 * p.qs + hk * NN, p.qs, GC, n, L::KB);
+    cp_commit();
+    float DQ[CT][4] = {}, DK[CT][4] = {};
+    for (int hg = 0; hg < group; ++hg) {
+        const int h = hk * group + hg;
+        float A[2][4] = {}, B[2][4] = {}, aq[CT][4] = {}, ak[CT][4] = {}, ao[CT][4] = {};
+        float ss = 0.f;
+        for (int sl = 0; sl < NN / DW; ++sl) {
+            const long long ye = t0 * p.H * NN + (long long)h * NN + sl * DW, ys = (long long)p.H * NN;
+            const long long se = ((slot * p.H + h) * NN + sl * DW) * NN;
+            __syncthreads();            // the last readers of what lies there
+            load_rows<DW, F32>(base + L::kY, static_cast<const Tin *>(p.dy) + ye, ys, GC, n, L::YB);
+            load_rows<DW, F32>(base + L::kE, static_cast<const Tin *>(p.keep_E) + ye, ys, GC, n, L::YB);
+            load_rows<DW, F32>(base + L::kX, static_cast<const Tin *>(p.dv) + ye, ys, GC, n, L::YB);
+            if constexpr (!F32) {
+                load_rows<DW, F32>(base + L::kE + L::YB, static_cast<const Tin *>(p.keep_E) + p.keep_lo + ye, ys, GC, n, L::YB);
+                load_rows<DW, F32>(base + L::kX + L::YB, static_cast<const Tin *>(p.keep_dlo) + ye, ys, GC, n, L::YB);
+                load_rows<NN, F32>(base + L::kS + L::SB, static_cast<const Tin *>(p.keep_S) + p.keep_second + se, NN, DW, DW, L::SB);
+                load_rows<NN, F32>(base + L::kD + L::SB, static_cast<const Tin *>(p.keep_dS) + p.keep_second + se, NN, DW, DW, L::SB);
+            }
+            load_rows<NN, F32>(base + L::kS, static_cast<const Tin *>(p.keep_S) + se, NN, DW, DW, L::SB);
+            load_rows<NN, F32>(base + L::kD, static_cast<const Tin *>(p.keep_dS) + se, NN, DW, DW, L::SB);
+            cp_commit();
+            cp_wait<0>();
+            __syncthreads();
+            if (sl == 0) {
+                if (hg == 0) {          // lengths: four threads per row, keys then queries
+                    const int row = (tid >> 2) & 63, part = tid & 3;
+                    const uint32_t at = base + (tid < 256 ? L::kK : L::kQ);
+                    float l = 0.f;
+#pragma unroll 4
+                    for (int c = 0; c < NN / 8; ++c) {
+                        const float2 v = pair_at<NB, TI>(at, L::KB, row, 8 * c + 2 * part);
+                        l = fmaf(v.x, v.x, fmaf(v.y, v.y, l));
+                    }
+                    l = quad_sum(l);
+                    l = p.qk_norm ? rsqrtf(l + p.norm_eps) : 1.f;
+                    if (part == 0) (tid < 256 ? sc->rk : sc->sq)[row] = tid < 256 ? l : l * p.scale;
+                    __syncthreads();
+                }
+                if (warp == 0) {        // the decays: two tokens per lane
+                    float g[2], b[2];
+                    long long G[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int i = 2 * lane + e;
+                        Gate<F32> gate;
+                        gate.load(p.g, p.beta, (t0 + i) * p.H + h, i < n);
+                        g[e] = delta_clamp(gate.num(gate.g));
+                        b[e] = gate.num(gate.beta);
+                        G[e] = llrintf(fminf(g[e], 120.f) * 4294967296.f);
+                    }
+                    const bool nan = __any_sync(0xffffffffu, g[0] != g[0] || g[1] != g[1]);
+                    const long long second = G[1];
+                    G[1] += G[0];
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const long long x = __shfl_up_sync(0xffffffffu, G[1], o);
+                        if (lane >= o) G[1] += x;
+                    }
+                    G[0] = G[1] - second;
+                    const long long last = __shfl_sync(0xffffffffu, G[1], 31);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int i = 2 * lane + e;
+                        const float bad = nan ? __int_as_float(0x7fffffff) : 0.f;
+                        const float in = expf(float(G[e]) * 2.3283064365386963e-10f) + bad;
+                        const float to = expf(float(last - G[e]) * 2.3283064365386963e-10f);
+                        sc->ghi[i] = float(int(G[e] >> 22)) * 9.765625e-4f + bad;
+                        sc->glo[i] = float(int(G[e] & 0x3fffff)) * 2.3283064365386963e-10f;
+                        sc->beta[i] = b[e];
+                        sc->kin[i] = in * sc->rk[i];
+                        sc->qin[i] = in * sc->sq[i];
+                        sc->kout[i] = to * sc->rk[i];
+                        sc->out[i] = to * sc->rk[i] * b[e];
+                        if (i == GC - 1) sc->whole = in;
+                    }
+                }
+            }
+            // A, B over the value channels; dY S, dX S, E dS'
+#pragma unroll 1
+            for (int ks = 0; ks < DW / 16; ++ks) {
+                uint32_t y[TI][4], x[TE][4], e[TE][4];
+#pragma unroll
+                for (int i = 0; i < TI; ++i) ldsm4(y[i], addr_a<YNB>(base + L::kY + i * L::YB, 16 * wr, ks));
+#pragma unroll
+                for (int i = 0; i < TE; ++i) {
+                    ldsm4(x[i], addr_a<YNB>(base + L::kX + i * L::YB, 16 * wr, ks));
+                    ldsm4(e[i], addr_a<YNB>(base + L::kE + i * L::YB, 16 * wr, ks));
+                }
+                if (wc <= wr) {         // tokens j of this warp's column group are not all behind its rows
+                    uint32_t b[TE][1][4];
+#pragma unroll
+                    for (int i = 0; i < TE; ++i) ldsm4(b[i][0], addr_b<YNB>(base + L::kE + i * L::YB, j0, ks));
+                    mma_terms<TI, TE, 2>(A, y, b);
+                    mma_terms<TE, TE, 2>(B, x, b);
+                }
+                uint32_t b[TE][CT / 2][4];
+#pragma unroll
+                for (int i = 0; i < TE; ++i)
+#pragma unroll
+                    for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kS + i * L::SB, 16 * ks, c0 / 8 + 2 * m));
+                mma_terms<TI, TE, CT>(aq, y, b);
+                mma_terms<TE, TE, CT>(ak, x, b);
+#pragma unroll
+                for (int i = 0; i < TE; ++i)
+#pragma unroll
+                    for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kD + i * L::SB, 16 * ks, c0 / 8 + 2 * m));
+                mma_terms<TE, TE, CT>(ao, e, b);
+            }
+            for (int i = tid; i < DW * NN / 2; i += GT) {       // <S, dS'>
+                const float2 a = pair_at<NB, TE>(base + L::kS, L::SB, i / (NN / 2), 2 * (i % (NN / 2)));
+                const float2 b = pair_at<NB, TE>(base + L::kD, L::SB, i / (NN / 2), 2 * (i % (NN / 2)));
+                ss = fmaf(a.x, b.x, fmaf(a.y, b.y, ss));
+            }
+        }
+        // the keys' and queries' products
+        float QK[2][4] = {}, KK[2][4] = {};
+        if (wc <= wr) {
+#pragma unroll 1
+            for (int ks = 0; ks < NN / 16; ++ks) {
+                uint32_t a[TI][4], d[TI][4], b[TI][1][4];
+#pragma unroll
+                for (int i = 0; i < TI; ++i) {
+                    ldsm4(a[i], addr_a<NB>(base + L::kQ + i * L::KB, 16 * wr, ks));
+                    ldsm4(d[i], addr_a<NB>(base + L::kK + i * L::KB, 16 * wr, ks));
+                    ldsm4(b[i][0], addr_b<NB>(base + L::kK + i * L::KB, j0, ks));
+                }
+                mma_terms<TI, TI, 2>(QK, a, b);
+                mma_terms<TI, TI, 2>(KK, d, b);
+            }
+        }
+        __syncthreads();                // the slice has been read, the scalars are there
+        // rows i = 16 wr + gr (+ 8), columns j = j0 + 8 m + 2 tc (+ 1)
+        float rows[2] = {}, tails[2] = {};
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const int j = j0 + 8 * m + 2 * tc;
+            float cols[2] = {};
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const int i = 16 * wr + gr + 4 * e;
+                float vn[2], vo[2];
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    const float d = fast_exp((sc->ghi[i] - sc->ghi[j + f]) + (sc->glo[i] - sc->glo[j + f])) * sc->rk[j + f];
+                    const float nn = j + f <= i ? A[m][e + f] * d * sc->sq[i] : 0.f, oo = j + f < i ? B[m][e + f] * d * sc->rk[i] : 0.f;
+                    const float z = nn * QK[m][e + f] - oo * KK[m][e + f], bt = sc->beta[j + f];
+                    cols[f] += z;
+                    rows[e >> 1] = fmaf(bt, z, rows[e >> 1]);
+                    vn[f] = nn * bt;
+                    vo[f] = -oo * bt;
+                }
+                uint32_t a[TE], b[TE];
+                split2<TE>(vn[0], vn[1], a);
+                split2<TE>(vo[0], vo[1], b);
+#pragma unroll
+                for (int z = 0; z < TE; ++z) {
+                    const uint32_t to = base + z * L::MB + tile<GC * 2>(i, j >> 3) + ((j & 7) << 1);
+                    st_b32(to + L::kN, a[z]);
+                    st_b32(to + L::kO, b[z]);
+                }
+            }
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                const float x = col_sum(cols[f]);
+                if (gr == 0) sc->col[wr][j + f] = x;
+            }
+        }
+        // what came through the states, over this warp's key channels
+#pragma unroll
+        for (int m = 0; m < CT; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const int i = 16 * wr + gr + 4 * e, c = c0 + 8 * m + 2 * tc;
+                const float2 qv = pair_at<NB, TI>(base + L::kQ, L::KB, i, c), kv = pair_at<NB, TI>(base + L::kK, L::KB, i, c);
+                const float qin = sc->qin[i], kin = sc->kin[i], ko = sc->kout[i], ou = sc->out[i];
+                const float q0 = qin * aq[m][e], q1 = qin * aq[m][e + 1], k0 = kin * ak[m][e], k1 = kin * ak[m][e + 1];
+                rows[e >> 1] += fmaf(qv.x, q0, qv.y * q1) - fmaf(kv.x, k0, kv.y * k1);
+                tails[e >> 1] += ko * fmaf(kv.x, ao[m][e], kv.y * ao[m][e + 1]);
+                DQ[m][e] += q0;
+                DQ[m][e + 1] += q1;
+                DK[m][e] += fmaf(ou, ao[m][e], -k0);
+                DK[m][e + 1] += fmaf(ou, ao[m][e + 1], -k1);
+            }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float x = quad_sum(rows[e]), y = quad_sum(tails[e]);
+            if (tc == 0) {
+                sc->row[wc][16 * wr + gr + 8 * e] = x;
+                sc->tail[wc][16 * wr + gr + 8 * e] = y;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (lane == 0) sc->ss[warp] = ss;
+        __syncthreads();
+        // sq dQ += n K, rk dK -= o K: depth j up to this row block
+#pragma unroll 1
+        for (int kb = 0; kb <= wr; ++kb) {
+            uint32_t a[TE][4], d[TE][4], b[TI][CT / 2][4];
+#pragma unroll
+            for (int i = 0; i < TE; ++i) {
+                ldsm4(a[i], addr_a<GC * 2>(base + L::kN + i * L::MB, 16 * wr, kb));
+                ldsm4(d[i], addr_a<GC * 2>(base + L::kO + i * L::MB, 16 * wr, kb));
+            }
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kK + i * L::KB, 16 * kb, c0 / 8 + 2 * m));
+            mma_terms<TE, TI, CT>(DQ, a, b);
+            mma_terms<TE, TI, CT>(DK, d, b);
+        }
+        // rk dK += n^T Q - o^T K: depth i from this row block on
+#pragma unroll 1
+        for (int ib = wr; ib < 4; ++ib) {
+            uint32_t a[TE][4], d[TE][4], b[TI][CT / 2][4];
+            const uint32_t at = tile<GC * 2>(16 * ib + (lane & 7) + ((lane >> 4) << 3), 2 * wr + ((lane >> 3) & 1));
+#pragma unroll
+            for (int i = 0; i < TE; ++i) {
+                ldsm4t(a[i], base + L::kN + i * L::MB + at);
+                ldsm4t(d[i], base + L::kO + i * L::MB + at);
+            }
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kQ + i * L::KB, 16 * ib, c0 / 8 + 2 * m));
+            mma_terms<TE, TI, CT>(DK, a, b);
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kK + i * L::KB, 16 * ib, c0 / 8 + 2 * m));
+            mma_terms<TE, TI, CT>(DK, d, b);
+        }
+        if (warp == 0) {                // dbeta and dg: two tokens per lane, sums in a fixed order
+            float db[2], dG[2], tail = 0.f, sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * lane + e;
+                const float t = (sc->tail[0][i] + sc->tail[1][i]) + (sc->tail[2][i] + sc->tail[3][i]);
+                db[e] = t + ((sc->col[0][i] + sc->col[1][i]) + (sc->col[2][i] + sc->col[3][i]));
+                dG[e] = ((sc->row[0][i] + sc->row[1][i]) + (sc->row[2][i] + sc->row[3][i])) - sc->beta[i] * db[e];
+                tail = fmaf(sc->beta[i], t, tail);
+            }
+            float x = lane < GT / 32 ? sc->ss[lane] : 0.f;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                x += __shfl_xor_sync(0xffffffffu, x, o);
+                tail += __shfl_xor_sync(0xffffffffu, tail, o);
+            }
+            sum = dG[0] + dG[1];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {      // over this lane's tokens and the later ones
+                const float z = __shfl_down_sync(0xffffffffu, sum, o);
+                if (lane + o < 32) sum += z;
+            }
+            const float last = fmaf(sc->whole, x, tail);
+            const float dg[2] = {sum + last, sum - dG[0] + last};
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (2 * lane + e < n) {
+                    const long long at = (t0 + 2 * lane + e) * p.H + h;
+                    if constexpr (F32) {
+                        static_cast<float *>(p.dg)[at] = dg[e];
+                        static_cast<float *>(p.dbeta)[at] = db[e];
+                    } else {
+                        static_cast<__nv_bfloat16 *>(p.dg)[at] = __float2bfloat16(dg[e]);
+                        static_cast<__nv_bfloat16 *>(p.dbeta)[at] = __float2bfloat16(db[e]);
+                    }
+                }
+        }
+    }
+    // back through the lengths, and out
+    if (p.qk_norm) {
+        float dq[2] = {}, dk[2] = {};
+#pragma unroll
+        for (int m = 0; m < CT; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const int i = 16 * wr + gr + 4 * e, c = c0 + 8 * m + 2 * tc;
+                const float2 qv = pair_at<NB, TI>(base + L::kQ, L::KB, i, c), kv = pair_at<NB, TI>(base + L::kK, L::KB, i, c);
+                dq[e >> 1] += fmaf(qv.x, DQ[m][e], qv.y * DQ[m][e + 1]);
+                dk[e >> 1] += fmaf(kv.x, DK[m][e], kv.y * DK[m][e + 1]);
+            }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float x = quad_sum(dq[e]), y = quad_sum(dk[e]);
+            if (tc == 0) {
+                sc->dq[wc][16 * wr + gr + 8 * e] = x;
+                sc->dk[wc][16 * wr + gr + 8 * e] = y;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < CT; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const int i = 16 * wr + gr + 4 * e, c = c0 + 8 * m + 2 * tc;
+                const float2 qv = pair_at<NB, TI>(base + L::kQ, L::KB, i, c), kv = pair_at<NB, TI>(base + L::kK, L::KB, i, c);
+                const float rq = sc->sq[i] / p.scale, rk = sc->rk[i];
+                const float fq = rq * rq * ((sc->dq[0][i] + sc->dq[1][i]) + (sc->dq[2][i] + sc->dq[3][i]));
+                const float fk = rk * rk * ((sc->dk[0][i] + sc->dk[1][i]) + (sc->dk[2][i] + sc->dk[3][i]));
+                DQ[m][e] = fmaf(-fq, qv.x, DQ[m][e]);
+                DQ[m][e + 1] = fmaf(-fq, qv.y, DQ[m][e + 1]);
+                DK[m][e] = fmaf(-fk, kv.x, DK[m][e]);
+                DK[m][e + 1] = fmaf(-fk, kv.y, DK[m][e + 1]);
+            }
+    }
+#pragma unroll
+    for (int m = 0; m < CT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+            const int i = 16 * wr + gr + 4 * e;
+            if (i >= n) continue;
+            const long long at = ((t0 + i) * p.Hk + hk) * NN + c0 + 8 * m + 2 * tc;
+            if constexpr (F32) {
+                *reinterpret_cast<float2 *>(static_cast<float *>(p.dq) + at) = make_float2(DQ[m][e], DQ[m][e + 1]);
+                *reinterpret_cast<float2 *>(static_cast<float *>(p.dk) + at) = make_float2(DK[m][e], DK[m][e + 1]);
+            } else {
+                *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.dq) + at) = pack(DQ[m][e], DQ[m][e + 1]);
+                *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.dk) + at) = pack(DK[m][e], DK[m][e + 1]);
+            }
+        }
+}
+
+}  // namespace
+
+// ---- host side ---------------------------------------------------------------------------------------
+
+cudaError_t allow_dynamic_smem(const void *kernel, int bytes);
+
+namespace {
+
+template <int NN, int RW, bool F32>
+cudaError_t launch_t(const DeltaArgs &p, long long slots) {
+    using R = RevLayout<NN, RW, F32>;
+    constexpr int grad_bytes = GradLayout<NN, F32>::kF + int(sizeof(GradScalars));
+    const void *rev = reinterpret_cast<const void *>(delta_reverse_kernel<NN, RW, F32>);
+    const void *grad = reinterpret_cast<const void *>(delta_grad_kernel<NN, F32>);
+    cudaError_t e = allow_dynamic_smem(rev, R::total);
+    if (e != cudaSuccess) return e;
+    e = allow_dynamic_smem(grad, grad_bytes);
+    if (e != cudaSuccess) return e;
+    e = launch_delta_states(p);
+    if (e != cudaSuccess) return e;
+    delta_reverse_kernel<NN, RW, F32><<<unsigned(p.B) * p.H * (NN / (16 * RW)), R::threads, R::total, p.stream>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    delta_grad_kernel<NN, F32><<<unsigned(slots) * p.Hk, GT, grad_bytes, p.stream>>>(p);
+    return cudaGetLastError();
+}
+
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+// Per row E (bf16: in two terms) and the second term of dv, per chunk of 64 S and dS (bf16: in two terms).
+size_t delta_backward_workspace(size_t rows, int B, int H, int N, wkv7_dtype dt) {
+    const size_t row = rows * H * N, state = (rows / 64 + B) * H * N * N;
+    return dt == WKV7_BF16 ? 3 * up(row * 2) + 4 * up(state * 2) : up(row * 4) + 2 * up(state * 4);
+}
+
+cudaError_t launch_delta_backward(const DeltaArgs &p0) {
+    DeltaArgs p = p0;
+    const size_t rows = p.cu ? size_t(p.T) : size_t(p.B) * p.T, el = p.dt == WKV7_BF16 ? 2 : 4;
+    const size_t row = up(rows * p.H * p.N * el), slots = rows / 64 + p.B, state = up(slots * p.H * p.N * p.N * el);
+    char *ws = static_cast<char *>(p.keep_E);
+    p.keep_lo = (long long)(row / el);
+    p.keep_dlo = ws + 2 * row;
+    ws += p.dt == WKV7_BF16 ? 3 * row : row;
+    p.keep_S = ws;
+    p.keep_dS = ws + (p.dt == WKV7_BF16 ? 2 : 1) * state;
+    p.keep_second = (long long)(state / el);
+    if (p.dt == WKV7_F32) return p.N == 64 ? launch_t<64, 4, true>(p, slots) : launch_t<128, 4, true>(p, slots);
+    return p.N == 64 ? launch_t<64, 4, false>(p, slots) : launch_t<128, 8, false>(p, slots);
+}
+
+}  // namespace wkv7

@@ -21,12 +21,14 @@ using namespace dm;
 
 namespace {
 
-template <int NN, int RW, bool F32>
+// STATES: the backward's forward sweep, which keeps the errors E and every second chunk's first state and
+// has no use for the queries.
+template <int NN, int RW, bool F32, bool STATES>
 struct Layout {
-    static constexpr int TI = F32 ? 3 : 1, TP = F32 ? 3 : 2;
+    static constexpr int TI = F32 ? 3 : 1, TP = STATES ? 0 : F32 ? 3 : 2;
     static constexpr int KB = TI * C * NN * 2;              // keys (and as much for queries)
     static constexpr int VB = F32 ? 0 : C * RW * 32;        // values of the CTA's rows; y on its way out
-    static constexpr int kK = 0, kQ = KB, kV = 2 * KB, kW = kV + VB, kP = kW + 3 * kTri, kS = kP + TP * kTri;
+    static constexpr int kK = 0, kQ = KB, kV = STATES ? KB : 2 * KB, kW = kV + VB, kP = kW + 3 * kTri, kS = kP + TP * kTri;
     static constexpr int stage = (kS + int(sizeof(Scalars)) + 127) / 128 * 128;
     // two chunks being prepared, one at work, and the rest loading: what two CTAs of N = 64 bf16, or one of
     // the others, have room for
@@ -59,9 +61,9 @@ __device__ __forceinline__ int first_bad(uint32_t mask, int r) {
     return min(at, __shfl_xor_sync(0xffffffffu, at, 2));
 }
 
-template <int NN, int RW, bool F32>
+template <int NN, int RW, bool F32, bool STATES>
 __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64) ? 2 : 1) delta_chunk_kernel(const DeltaArgs p) {
-    using L = Layout<NN, RW, F32>;
+    using L = Layout<NN, RW, F32, STATES>;
     using Tin = std::conditional_t<F32, float, __nv_bfloat16>;
     constexpr int TI = L::TI, TP = L::TP, TS = F32 ? 3 : 2, NB = NN * 2, TB = C * NB, VNB = RW * 32;
     extern __shared__ __align__(128) unsigned char sm[];
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
             const int n = int(min((long long)C, t1 - t0 - (long long)c * C));
             next.load(p.g, p.beta, (t0 + (long long)c * C + lane) * p.H + h, lane < n);
             k.load(st + L::kK, n);
-            q.load(st + L::kQ, n);
+            if constexpr (!STATES) q.load(st + L::kQ, n);
             if constexpr (!F32) v.load(st + L::kV, n);
             k.advance(kGroups);
             q.advance(kGroups);
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
             const bool queries = ((warp ^ (c / kGroups)) & 1) != 0;
             Scalars *sc = reinterpret_cast<Scalars *>(st + L::kS);
             const float g = delta_clamp(gate.num(gate.g)), bt = gate.num(gate.beta);
-            prepare_chunk<NN, TI, TP>(sa + L::kK, sa + L::kQ, sa + L::kW, sa + L::kP, sc, ps, p, g, bt, queries, 1 + group);
+            prepare_chunk<NN, TI, TP>(sa + L::kK, sa + L::kQ, st + L::kW, sa + L::kP, sc, ps, p, g, bt, queries, 1 + group);
             bar_arrive(full + c % L::stages, L::meet);
         }
         return;
@@ -131,7 +133,8 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
         }
         S[n][0] = a.x; S[n][1] = a.y; S[n][2] = b.x; S[n][3] = b.y;
     }
-    Tin *y = static_cast<Tin *>(p.y) + size_t(h) * NN + row;
+    Tin *y = static_cast<Tin *>(STATES ? p.keep_E : p.y) + size_t(h) * NN + row;
+    [[maybe_unused]] const long long slot0 = delta_slot(t0, s);
     const Tin *vrow = static_cast<const Tin *>(p.v) + size_t(h) * NN + row;
     const size_t ys = size_t(p.H) * NN;
     for (int c = 0; c < chunks; ++c) {
@@ -150,6 +153,9 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
                     const int i = 8 * n + 2 * tc + (e & 1);
                     V[n][e] = i < n_tok ? __ldg(vrow + (t + i) * p.vs + gr + 8 * (e >> 1)) : 0.f;
                 }
+        }
+        if constexpr (STATES) {         // what the grads' chunks of 64 tokens start from
+            if (c % 2 == 0) keep_state<F32, NN>(p.keep_S, p.keep_second, (slot0 + c / 2) * p.H + h, row, S);
         }
         bar_sync(full + c % L::stages, L::meet);
         float z = 0.f;
@@ -191,18 +197,20 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
 #pragma unroll
                     for (int n = 0; n < 4; ++n) mma(X[n], a[x], b[z][n >> 1][2 * (n & 1)], b[z][n >> 1][2 * (n & 1) + 1]);
                 }
+            if constexpr (!STATES) {
 #pragma unroll
-            for (int i = 0; i < TI; ++i)
+                for (int i = 0; i < TI; ++i)
 #pragma unroll
-                for (int n = 0; n < 2; ++n) ldsm4(b[i][n], addr_b<NB>(st + L::kQ + i * TB, 16 * n, ks));
+                    for (int n = 0; n < 2; ++n) ldsm4(b[i][n], addr_b<NB>(st + L::kQ + i * TB, 16 * n, ks));
 #pragma unroll
-            for (int x = TS - 1; x >= 0; --x)
+                for (int x = TS - 1; x >= 0; --x)
 #pragma unroll
-                for (int z = TI - 1; z >= 0; --z) {
-                    if (x + z > TS - 1) continue;
+                    for (int z = TI - 1; z >= 0; --z) {
+                        if (x + z > TS - 1) continue;
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) mma(Y[n], a[x], b[z][n >> 1][2 * (n & 1)], b[z][n >> 1][2 * (n & 1) + 1]);
-                }
+                        for (int n = 0; n < 4; ++n) mma(Y[n], a[x], b[z][n >> 1][2 * (n & 1)], b[z][n >> 1][2 * (n & 1) + 1]);
+                    }
+            }
         }
         if constexpr (!F32) {
 #pragma unroll
@@ -216,11 +224,12 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const float2 in = *reinterpret_cast<const float2 *>(&sc->kin[8 * n + 2 * tc]);
-            const float2 qn = *reinterpret_cast<const float2 *>(&sc->qin[8 * n + 2 * tc]);
+            float2 qn;
+            if constexpr (!STATES) qn = *reinterpret_cast<const float2 *>(&sc->qin[8 * n + 2 * tc]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 X[n][e] = fmaf(-(e & 1 ? in.y : in.x), X[n][e], V[n][e]);
-                Y[n][e] *= e & 1 ? qn.y : qn.x;
+                if constexpr (!STATES) Y[n][e] *= e & 1 ? qn.y : qn.x;
             }
         }
         uint32_t bad = 0;
@@ -246,14 +255,20 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
             }
         }
         if (careful) take_out(E, bad);
+        if constexpr (STATES) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) Y[n][e] = E[n][e];
+        }
         // Y^T += E^T P^T
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
+        for (int kb = 0; kb < (STATES ? 0 : 2); ++kb) {
             uint32_t a[TS][4];
             split_a<TS>(E[2 * kb], E[2 * kb + 1], a);
 #pragma unroll
             for (int ib = kb; ib < 2; ++ib) {
-                uint32_t w[TP][4];
+                uint32_t w[TP > 0 ? TP : 1][4];
 #pragma unroll
                 for (int z = 0; z < TP; ++z) ldsm4(w[z], addr_block(st + L::kP + z * kTri + (ib + kb) * 512));
 #pragma unroll
@@ -320,27 +335,37 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
                     if (i < n_tok) y[(t + i) * ys + gr + 8 * (e >> 1)] = Y[n][e];
                 }
         } else {                // through the values' place (this warp's own columns) to whole 32-byte pieces
-            __syncwarp();
+            auto put = [&](Tin *to) {
+                __syncwarp();
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                uint32_t r[4];
+                for (int m = 0; m < 2; ++m) {
+                    uint32_t r[4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    r[2 * i] = pack(Y[2 * m + i][0], Y[2 * m + i][1]);
-                    r[2 * i + 1] = pack(Y[2 * m + i][2], Y[2 * m + i][3]);
+                    for (int i = 0; i < 2; ++i) {
+                        r[2 * i] = pack(Y[2 * m + i][0], Y[2 * m + i][1]);
+                        r[2 * i + 1] = pack(Y[2 * m + i][2], Y[2 * m + i][3]);
+                        if constexpr (STATES) {         // what the rounding leaves
+                            Y[2 * m + i][0] -= lo_f(r[2 * i]);
+                            Y[2 * m + i][1] -= hi_f(r[2 * i]);
+                            Y[2 * m + i][2] -= lo_f(r[2 * i + 1]);
+                            Y[2 * m + i][3] -= hi_f(r[2 * i + 1]);
+                        }
+                    }
+                    const int tok = 16 * m + (lane & 7) + ((lane >> 4) << 3);
+                    stsm4t(st + L::kV + tile<VNB>(tok, 2 * warp + ((lane >> 3) & 1)), r);
                 }
-                const int tok = 16 * m + (lane & 7) + ((lane >> 4) << 3);
-                stsm4t(st + L::kV + tile<VNB>(tok, 2 * warp + ((lane >> 3) & 1)), r);
-            }
-            __syncwarp();
+                __syncwarp();
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int tok = 16 * m + (lane >> 1);
-                uint4 r;
-                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                             : "r"(st + L::kV + tile<VNB>(tok, 2 * warp + (lane & 1))) : "memory");
-                if (tok < n_tok) *reinterpret_cast<uint4 *>(y + (t + tok) * ys + 8 * (lane & 1)) = r;
-            }
+                for (int m = 0; m < 2; ++m) {
+                    const int tok = 16 * m + (lane >> 1);
+                    uint4 r;
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                                 : "r"(st + L::kV + tile<VNB>(tok, 2 * warp + (lane & 1))) : "memory");
+                    if (tok < n_tok) *reinterpret_cast<uint4 *>(to + (t + tok) * ys + 8 * (lane & 1)) = r;
+                }
+            };
+            put(y);
+            if constexpr (STATES) put(y + p.keep_lo);   // the errors in two bf16 terms
         }
         if (c + L::stages < chunks) bar_arrive(empty + c % L::stages, L::meet);
     }
@@ -361,22 +386,26 @@ cudaError_t allow_dynamic_smem(const void *kernel, int bytes);
 
 namespace {
 
-template <int NN, int RW, bool F32>
+template <int NN, int RW, bool F32, bool STATES>
 cudaError_t launch_t(const DeltaArgs &p) {
-    using L = Layout<NN, RW, F32>;
-    const void *kernel = reinterpret_cast<const void *>(delta_chunk_kernel<NN, RW, F32>);
+    using L = Layout<NN, RW, F32, STATES>;
+    const void *kernel = reinterpret_cast<const void *>(delta_chunk_kernel<NN, RW, F32, STATES>);
     const cudaError_t e = allow_dynamic_smem(kernel, L::total);
     if (e != cudaSuccess) return e;
-    delta_chunk_kernel<NN, RW, F32><<<unsigned(p.B) * p.H * (NN / (16 * RW)), L::threads, L::total, p.stream>>>(p);
+    delta_chunk_kernel<NN, RW, F32, STATES><<<unsigned(p.B) * p.H * (NN / (16 * RW)), L::threads, L::total, p.stream>>>(p);
     return cudaGetLastError();
+}
+
+template <bool STATES>
+cudaError_t launch(const DeltaArgs &p) {
+    const bool f32 = p.dt == WKV7_F32;
+    if (p.N == 64) return f32 ? launch_t<64, 4, true, STATES>(p) : launch_t<64, 4, false, STATES>(p);
+    return f32 ? launch_t<128, 4, true, STATES>(p) : launch_t<128, 8, false, STATES>(p);
 }
 
 }  // namespace
 
-cudaError_t launch_delta_forward(const DeltaArgs &p) {
-    const bool f32 = p.dt == WKV7_F32;
-    if (p.N == 64) return f32 ? launch_t<64, 4, true>(p) : launch_t<64, 4, false>(p);
-    return f32 ? launch_t<128, 4, true>(p) : launch_t<128, 8, false>(p);
-}
+cudaError_t launch_delta_forward(const DeltaArgs &p) { return launch<false>(p); }
+cudaError_t launch_delta_states(const DeltaArgs &p) { return launch<true>(p); }
 
 }  // namespace wkv7

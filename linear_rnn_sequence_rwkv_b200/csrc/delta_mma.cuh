@@ -24,7 +24,9 @@ constexpr int C = 32;               // tokens per chunk
 constexpr int kGroup = 64;          // threads that prepare one chunk: a warp for the keys, one for the queries
 constexpr int kGroups = 2;          // chunks prepared at a time
 constexpr int kTri = 3 * 512;       // bytes of one term of a lower triangular [32][32]: blocks (0,0), (1,0), (1,1)
-constexpr int kAs = 20;             // row of a 16 x 16 fp32 scratch block
+constexpr int kAs = 20;             // row of a 16 x 16 fp32 scratch block, two of which lie where W goes
+constexpr int kAb = 16 * kAs + 16;  // from one block to the next, in other banks
+static_assert(2 * kAb * 4 <= 3 * kTri, "the scratch blocks fit W's place");
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -95,9 +97,11 @@ __device__ __forceinline__ void split_a(const float (&u)[4], const float (&v)[4]
         for (int j = 0; j < 4; ++j) a[i][j] = r[j][i];
 }
 
-// Byte offset of 16-byte chunk c of row r in a tile of rows of NB bytes (a multiple of 128): eight rows
+// Byte offset of 16-byte chunk c of row r in a tile of rows of NB bytes (64 or a multiple of 128): eight rows
 // of one chunk column lie in eight different bank groups.
-template <int NB> __device__ __forceinline__ uint32_t tile(int r, int c) { return uint32_t(r * NB + ((c ^ (r & 7)) << 4)); }
+template <int NB> __device__ __forceinline__ uint32_t tile(int r, int c) {
+    return uint32_t(r * NB + ((NB == 64 ? c ^ ((r >> 1) & 3) : c ^ (r & 7)) << 4));
+}
 // The same inside a 16 x 16 block of bf16 (rows of 32 bytes).
 __device__ __forceinline__ uint32_t block(int r, int c) { return uint32_t(r * 32 + ((c ^ ((r >> 2) & 1)) << 4)); }
 
@@ -138,9 +142,8 @@ struct Scalars {
     float pad[2];
 };
 
-// Scratch of one preparing group.
+// What the two warps of a preparing group exchange.
 struct PrepScratch {
-    float A[2][16 * kAs + 16];      // the diagonal blocks of A by columns, then of W by rows
     float rk[C], rq[C];
 };
 
@@ -224,15 +227,18 @@ __device__ __forceinline__ float fast_exp(float x) { return __expf(x); }
 // Substitution over all 32 rows took 496 products in a row of straight-line code, and the
 // warps of both kinds then waited for instructions: code size is what this routine is written for, and
 // why its loop over the depth stays a loop.
+// TP = 0: neither P nor anything of the queries is wanted (the warp of the queries writes the scalars).
 template <int NN, int TI, int TP>
-__device__ __forceinline__ void prepare_chunk(uint32_t k, uint32_t q, uint32_t w_out, uint32_t p_out, Scalars *sc, PrepScratch *ps,
+__device__ __forceinline__ void prepare_chunk(uint32_t k, uint32_t q, unsigned char *w_at, uint32_t p_out, Scalars *sc, PrepScratch *ps,
                                               const DeltaArgs &p, float g, float beta, bool queries, int bar) {
     constexpr int NB = NN * 2, TB = C * NB;
     const int lane = threadIdx.x & 31, gr = lane >> 2, tc = lane & 3;
-    const uint32_t left = queries ? q : k;
+    const uint32_t left = queries ? q : k, w_out = smem_addr(w_at);
+    float *scratch = reinterpret_cast<float *>(w_at);
     // products with the keys, tiles (m, n): (0, 0), (0, 1), (1, 0), (1, 1), (1, 2), (1, 3)
     float acc[6][4] = {};
     float len[4] = {};
+    if (TP > 0 || !queries) {
 #pragma unroll 1
     for (int ks = 0; ks < NN / 16; ++ks) {
         uint32_t a0[TI][4], a1[TI][4], b0[TI][4], b1[TI][4];
@@ -274,6 +280,7 @@ __device__ __forceinline__ void prepare_chunk(uint32_t k, uint32_t q, uint32_t w
         len[r] += __shfl_xor_sync(0xffffffffu, len[r], 1);
         len[r] += __shfl_xor_sync(0xffffffffu, len[r], 2);
     }
+    }
     if (!queries) {
         const bool fine = len[0] + len[1] + len[2] + len[3] < INFINITY && g <= 80.f && fabsf(beta) < INFINITY;
         const bool odd = __any_sync(0xffffffffu, !fine);
@@ -281,7 +288,7 @@ __device__ __forceinline__ void prepare_chunk(uint32_t k, uint32_t q, uint32_t w
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) len[r] = (p.qk_norm ? rsqrtf(len[r] + p.norm_eps) : 1.f) * (queries ? p.scale : 1.f);
-    if (tc == 0) {
+    if (tc == 0 && (TP > 0 || !queries)) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) (queries ? ps->rq : ps->rk)[gr + 8 * r] = len[r];
     }
@@ -304,11 +311,12 @@ __device__ __forceinline__ void prepare_chunk(uint32_t k, uint32_t q, uint32_t w
         const float in = seen ? bad : expf(float(G) * 2.3283064365386963e-10f);
         const float out = (nan ? bad : expf(float(rest) * 2.3283064365386963e-10f)) * rk;
         sc->kin[lane] = in * rk;
-        sc->qin[lane] = in * ps->rq[lane];
+        if constexpr (TP > 0) sc->qin[lane] = in * ps->rq[lane];
         sc->kout[lane] = out;
         sc->out[lane] = out * beta;
         sc->beta[lane] = beta;
         if (lane == 31) sc->whole = nan ? bad : in;
+        if constexpr (TP == 0) return;
     }
     {   // D and the factors of rows and columns: rows gr + 8 i, columns 8 n + 2 tc, + 1
         float rh[4], rl[4], ch[8], cl[8], cb[8];
@@ -342,7 +350,7 @@ __device__ __forceinline__ void prepare_chunk(uint32_t k, uint32_t q, uint32_t w
             const int m = x < 2 ? 0 : 1, n = x < 2 ? x : x - 2;
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
-                uint32_t r[TP];
+                uint32_t r[TP > 0 ? TP : 1];
                 split2<TP>(acc[x][e], acc[x][e + 1], r);
 #pragma unroll
                 for (int z = 0; z < TP; ++z) st_b32(p_out + z * kTri + (m + (n >> 1)) * 512 + block(gr + 4 * e, n & 1) + 4 * tc, r[z]);
@@ -356,10 +364,10 @@ __device__ __forceinline__ void prepare_chunk(uint32_t k, uint32_t q, uint32_t w
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) ps->A[b][(8 * n + 2 * tc + (e & 1)) * kAs + gr + 8 * (e >> 1)] = acc[4 * b + n][e];
+            for (int e = 0; e < 4; ++e) scratch[b * kAb + (8 * n + 2 * tc + (e & 1)) * kAs + gr + 8 * (e >> 1)] = acc[4 * b + n][e];
     __syncwarp();
     const int col = lane & 15;
-    float *D = ps->A[lane >> 4];
+    float *D = scratch + (lane >> 4) * kAb;
     float t[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) t[i] = i == col ? 1.f : 0.f;
@@ -380,14 +388,17 @@ __device__ __forceinline__ void prepare_chunk(uint32_t k, uint32_t q, uint32_t w
 #pragma unroll
     for (int i = 0; i < 16; ++i) D[i * kAs + col] = t[i];
     __syncwarp();
+    float4 own[4];                  // row `col` of this half-warp's block
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {   // row `col` of this half-warp's block
-        const float4 x = *reinterpret_cast<const float4 *>(&D[col * kAs + 8 * c]), y = *reinterpret_cast<const float4 *>(&D[col * kAs + 8 * c + 4]);
+    for (int c = 0; c < 4; ++c) own[c] = *reinterpret_cast<const float4 *>(&D[col * kAs + 4 * c]);
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
         uint32_t w[4][3];
-        split2<3>(x.x, x.y, w[0]);
-        split2<3>(x.z, x.w, w[1]);
-        split2<3>(y.x, y.y, w[2]);
-        split2<3>(y.z, y.w, w[3]);
+        split2<3>(own[2 * c].x, own[2 * c].y, w[0]);
+        split2<3>(own[2 * c].z, own[2 * c].w, w[1]);
+        split2<3>(own[2 * c + 1].x, own[2 * c + 1].y, w[2]);
+        split2<3>(own[2 * c + 1].z, own[2 * c + 1].w, w[3]);
 #pragma unroll
         for (int z = 0; z < 3; ++z)
             st_v4(w_out + z * kTri + (lane >> 4) * 1024 + block(col, c), w[0][z], w[1][z], w[2][z], w[3][z]);
@@ -444,6 +455,28 @@ __device__ __forceinline__ void prepare_chunk(uint32_t k, uint32_t q, uint32_t w
     }
     __syncwarp();
     put(r, true);
+}
+
+// A warp's 16 rows of a state to a workspace's [unit][N][N]: as fp32, or for bf16 inputs as two bf16 terms
+// in arrays `second` elements apart.
+template <bool F32, int NN>
+__device__ __forceinline__ void keep_state(void *ws, long long second, long long unit, int row, const float (&S)[NN / 8][4]) {
+    const int gr = (threadIdx.x & 31) >> 2, tc = threadIdx.x & 3;
+    const size_t at = (size_t(unit) * NN + row + gr) * NN + 2 * tc;
+#pragma unroll
+    for (int n = 0; n < NN / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if constexpr (F32) {
+                *reinterpret_cast<float2 *>(static_cast<float *>(ws) + at + 8 * e * NN + 8 * n) = make_float2(S[n][2 * e], S[n][2 * e + 1]);
+            } else {
+                uint32_t r[2];
+                split2<2>(S[n][2 * e], S[n][2 * e + 1], r);
+                __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(ws) + at + 8 * e * NN + 8 * n;
+                *reinterpret_cast<uint32_t *>(to) = r[0];
+                *reinterpret_cast<uint32_t *>(to + second) = r[1];
+            }
+        }
 }
 
 }  // namespace dm

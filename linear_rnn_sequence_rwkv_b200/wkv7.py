@@ -37,7 +37,7 @@ EXPORTED = ("wkv7_opts_default", "wkv7_forward", "wkv7_decode_step", "wkv7_works
             "wkv7_probe_tf32_mma", "wkv7_forward_host", "wkv7_forward_host_workspace_bytes", "wkv7_epilogue",
             "wkv7_epilogue_backward", "wkv7_epilogue_backward_workspace_bytes", "wkv7_decode_step_ex",
             "wkv7_decode_step_raw", "wkv7_delta_opts_default", "wkv7_delta_forward", "wkv7_delta_step",
-            "wkv7_beam_select", "wkv7_beam_select_workspace_bytes", "wkv7_beam_reorder")
+            "wkv7_delta_backward", "wkv7_delta_backward_workspace_bytes", "wkv7_beam_select", "wkv7_beam_select_workspace_bytes", "wkv7_beam_reorder")
 
 
 class Wkv7Error(RuntimeError):
@@ -151,6 +151,10 @@ def load():
         lib.wkv7_delta_opts_default.restype = None
         lib.wkv7_delta_forward.argtypes = [ci] * 6 + [vp] * 8 + [dop, vp]
         lib.wkv7_delta_forward.restype = ci
+        lib.wkv7_delta_backward.argtypes = [ci] * 6 + [vp] * 14 + [dop, vp, csz, vp]
+        lib.wkv7_delta_backward.restype = ci
+        lib.wkv7_delta_backward_workspace_bytes.argtypes = [ci] * 6 + [dop]
+        lib.wkv7_delta_backward_workspace_bytes.restype = csz
         lib.wkv7_delta_step.argtypes = [ci] * 5 + [vp] * 6 + [ci, vp, vp, dop, vp]
         lib.wkv7_delta_step.restype = ci
         lib.wkv7_beam_select_workspace_bytes.argtypes = [ci] * 4
@@ -725,6 +729,46 @@ def delta_forward(q, k, v, g, beta, S0=None, *, scale=None, qk_norm=False, norm_
                                        _ptr(y), _ptr(S_T), ctypes.byref(o), handle)
     _check(st, "wkv7_delta_forward")
     return y, S_T
+
+
+DELTA_GRAD_NAMES = ("dq", "dk", "dv", "dg", "dbeta")
+
+
+def delta_backward(q, k, v, g, beta, dy, S0=None, dS_T=None, *, scale=None, qk_norm=False, norm_eps=1e-6,
+                   cu_seqlens=None, grads=None, dS0=None, return_state_grad=True, workspace=None, stream=None):
+    """Gradients of <dy, y> + <dS_T, S_T> for ``delta_forward``'s inputs (wkv7_delta_backward), with
+    the same options. dy like v; dS_T like S0. Returns a dict of dq, dk, dv, dg, dbeta (of the inputs'
+    type, dense) and dS0 (fp32; None if return_state_grad is False; may be dS_T). Rows behind the last
+    packed sequence are not written; without ``grads`` of the caller's they are zeros."""
+    lead = 2 if cu_seqlens is None else 1
+    shape, H, Hk, N, dt, o = _delta_args(q, k, v, g, beta, scale, qk_norm, norm_eps, cu_seqlens, lead)
+    B, T = shape if cu_seqlens is None else (cu_seqlens.numel() - 1, shape[0])
+    dev, states = v.device, (B, H, N, N)
+    _plain("dy", dy, v.shape, v.dtype, dev)
+    for name, t in (("S0", S0), ("dS_T", dS_T)):
+        if t is not None:
+            _plain(name, t, states, torch.float32, dev)
+    lib = load()
+    with _on(dev, stream) as handle:
+        like = {"dq": q.shape, "dk": k.shape, "dv": v.shape, "dg": g.shape, "dbeta": beta.shape}
+        if grads is None:
+            new = torch.empty if cu_seqlens is None else torch.zeros
+            grads = {n: new(s, device=dev, dtype=v.dtype) for n, s in like.items()}
+        for n, s in like.items():
+            _plain(n, grads[n], s, v.dtype, dev)
+        if dS0 is None and return_state_grad:
+            dS0 = torch.empty(states, device=dev, dtype=torch.float32)
+        if dS0 is not None:
+            _plain("dS0", dS0, states, torch.float32, dev)
+        need = int(lib.wkv7_delta_backward_workspace_bytes(B, T, H, Hk, N, dt, ctypes.byref(o)))
+        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+            workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        st = lib.wkv7_delta_backward(B, T, H, Hk, N, dt, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0),
+                                     _ptr(dy), _ptr(dS_T), *(_ptr(grads[n]) for n in DELTA_GRAD_NAMES), _ptr(dS0),
+                                     ctypes.byref(o), _ptr(workspace), ws_bytes, handle)
+    _check(st, "wkv7_delta_backward")
+    return {**{n: grads[n] for n in DELTA_GRAD_NAMES}, "dS0": dS0}
 
 
 def delta_step(q, k, v, g, beta, S, *, slots=None, scale=None, qk_norm=False, norm_eps=1e-6, y=None, stream=None):

@@ -35,6 +35,11 @@ def _fwd(lib, ptrs=None, B=1, T=4, H=2, Hk=1, N=64, dt=1, **opts):
     return lib.wkv7_delta_forward(B, T, H, Hk, N, dt, *p, ctypes.byref(_opts(**opts)), None)
 
 
+def _bwd(lib, ptrs=None, B=1, T=4, H=2, Hk=1, N=64, dt=1, ws_bytes=1 << 22, **opts):
+    p = _ptrs(("q", "k", "v", "g", "beta", "S0", "dy", "dS_T", "dq", "dk", "dv", "dg", "dbeta", "dS0", "workspace"), ptrs)
+    return lib.wkv7_delta_backward(B, T, H, Hk, N, dt, *p[:14], ctypes.byref(_opts(**opts)), p[14], ws_bytes, None)
+
+
 def _step(lib, ptrs=None, B=1, H=2, Hk=1, N=64, dt=1, n_slots=4, **opts):
     p = _ptrs(("q", "k", "v", "g", "beta", "S", "slots", "y"), ptrs)
     return lib.wkv7_delta_step(B, H, Hk, N, dt, *p[:6], n_slots, *p[6:], ctypes.byref(_opts(**opts)), None)
@@ -75,6 +80,34 @@ def test_forward_refusals(lib):
     assert _fwd(lib, ptrs={"S_T": BASE + 6 * STEP + 64}) == wkv7.ERR_ARG and b"overlaps" in lib.wkv7_last_error()
     assert _fwd(lib, ptrs={"S_T": BASE + 2 * STEP}) == wkv7.ERR_ARG
     assert _fwd(lib, cu_seqlens=BASE + 4) == wkv7.ERR_ALIGN and b"cu_seqlens" in lib.wkv7_last_error()
+
+
+@pytest.mark.parametrize("kw,status,word", [c for c in SIZES if "y" not in c[0].get("ptrs", {})])
+def test_backward_refusals_as_forward(lib, kw, status, word):
+    assert _bwd(lib, **kw) == status
+    assert word in lib.wkv7_last_error()
+
+
+def test_backward_refusals(lib):
+    for n in ("dy", "dq", "dk", "dv", "dg", "dbeta"):
+        assert _bwd(lib, ptrs={n: None}) == wkv7.ERR_ARG and n.encode() in lib.wkv7_last_error()
+    assert _bwd(lib, ws_bytes=16) == wkv7.ERR_WORKSPACE
+    assert _bwd(lib, ptrs={"workspace": None}) == wkv7.ERR_WORKSPACE
+    assert _bwd(lib, ptrs={"dv": BASE + 7 * STEP}) == wkv7.ERR_ARG and b"overlaps" in lib.wkv7_last_error()   # on dy
+    assert _bwd(lib, ptrs={"dS0": BASE + 8 * STEP + 64}) == wkv7.ERR_ARG                                        # across dS_T
+    assert _bwd(lib, ptrs={"dbeta": BASE + 15 * STEP}) == wkv7.ERR_ARG                                          # in the workspace
+    assert _bwd(lib, T=-1) == wkv7.ERR_ARG
+
+
+def test_backward_workspace(lib):
+    """E in two bf16 terms and dv's second per row and head, two states in two bf16 terms each per chunk
+    of 64 (one more per sequence); fp32 keeps E and the states as they are."""
+    f = lib.wkv7_delta_backward_workspace_bytes
+    assert f(2, 100, 4, 2, 64, 1, None) == 3 * 200 * 4 * 64 * 2 + 4 * 5 * 4 * 4096 * 2
+    assert f(2, 100, 4, 2, 64, 0, None) == 200 * 4 * 64 * 4 + 2 * 5 * 4 * 4096 * 4
+    o = _opts(cu_seqlens=BASE)
+    assert f(3, 100, 4, 2, 128, 1, ctypes.byref(o)) == 3 * 100 * 4 * 128 * 2 + 4 * 4 * 4 * 16384 * 2
+    assert f(2, 0, 4, 2, 64, 1, None) == 0 and f(2, 10, 3, 2, 64, 1, None) == 0
 
 
 def test_step_refusals(lib):
