@@ -11,8 +11,8 @@
 //          sq dQ = n K + qin (dY S),    rk dK = n^T Q - o K - o^T K + out (E dS') - kin (dX S)
 //          z = (n (Q K^T) - o (K K^T)) / beta_j,   tail_j = kout_j k_j.(E dS')_j
 //          dbeta_j = sum_i z_ij + tail_j
-//          dG_i = sum_j beta_j z_ij + q_i.(qin dY S)_i - k_i.(kin dX S)_i - beta_i dbeta_i
-//          dg_t = sum_{i >= t} dG_i + sum_j beta_j tail_j + exp(G_C) <S, dS'>
+//          dG_i = sum_{j<i} beta_j z_ij - beta_i sum_{j>i} z_ji + q_i.(qin dY S)_i - k_i.(kin dX S)_i
+//          dg_t = sum_{i >= t} dG_i + sum_{j < t} beta_j tail_j + exp(G_C) <S, dS'>
 //      (rk, sq: 1 / |k| and scale / |q|; with unit keys dk = rk dK - k^ (k^.rk dK), and q alike).
 //      The value heads of one key head are summed in the same accumulators, in order.
 // Precision: the chain of dS keeps three bf16 terms wherever a state or its gradient is read or written. For
@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
         if (r == 0 || c % 2 == 1) keep_state<F32, NN>(p.keep_dS, p.keep_second, (slot0 + c / 2) * p.H + h, row, S);
         bar_sync(full + r % L::stages, L::meet);
         // dE^T = out (dS K^T) + dY^T P
-        float E[4][4] = {};
+        Acc<F32, 4> ea, xa;
+        float (&E)[4][4] = ea.d, (&X)[4][4] = xa.d;
 #pragma unroll
         for (int ks = 0; ks < NN / 16; ++ks) {
             uint32_t a[3][4], b[TI][2][4];
@@ -137,9 +138,10 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
                 for (int z = TI - 1; z >= 0; --z) {
                     if (x + z > 2) continue;
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) mma(E[n], a[x], b[z][n >> 1][2 * (n & 1)], b[z][n >> 1][2 * (n & 1) + 1]);
+                    for (int n = 0; n < 4; ++n) ea.add(n, x + z == 0, a[x], b[z][n >> 1][2 * (n & 1)], b[z][n >> 1][2 * (n & 1) + 1]);
                 }
         }
+        ea.join();
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const float2 o = *reinterpret_cast<const float2 *>(&sc->out[8 * n + 2 * tc]);
@@ -160,13 +162,13 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
                 for (int x = TI - 1; x >= 0; --x)
 #pragma unroll
                     for (int z = 2 - x; z >= 0; --z) {
-                        mma(E[2 * jb], y[ib][x], w[z][0], w[z][1]);
-                        mma(E[2 * jb + 1], y[ib][x], w[z][2], w[z][3]);
+                        ea.add(2 * jb, x + z == 0, y[ib][x], w[z][0], w[z][1]);
+                        ea.add(2 * jb + 1, x + z == 0, y[ib][x], w[z][2], w[z][3]);
                     }
             }
         }
+        ea.join();
         // dX^T = dE^T W
-        float X[4][4] = {};
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             uint32_t a[3][4];
@@ -180,57 +182,62 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
                 for (int x = 2; x >= 0; --x)
 #pragma unroll
                     for (int z = 2 - x; z >= 0; --z) {
-                        mma(X[2 * jb], a[x], w[z][0], w[z][1]);
-                        mma(X[2 * jb + 1], a[x], w[z][2], w[z][3]);
+                        xa.add(2 * jb, x + z == 0, a[x], w[z][0], w[z][1]);
+                        xa.add(2 * jb + 1, x + z == 0, a[x], w[z][2], w[z][3]);
                     }
             }
         }
-        // dS <- exp(G_C) dS + (qin dY)^T Q - (kin dX)^T K
+        xa.join();
+        // dS <- exp(G_C) dS + (qin dY)^T Q - (kin dX)^T K: each sum on its own, small products first
         const float whole = sc->whole;
 #pragma unroll
-        for (int n = 0; n < NN / 8; ++n)
+        for (int part = 0; part < 2; ++part) {
+            uint32_t u[2][3][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) S[n][e] *= whole;
+            for (int kb = 0; kb < 2; ++kb) {
+                float w[2][4];
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            uint32_t a[3][4], d[3][4];
-            float u[2][4], w[2][4];
+                for (int n = 0; n < 2; ++n) {
+                    const float2 f = *reinterpret_cast<const float2 *>(&(part ? sc->kin : sc->qin)[16 * kb + 8 * n + 2 * tc]);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const float2 f = *reinterpret_cast<const float2 *>(&sc->qin[16 * kb + 8 * n + 2 * tc]);
-                const float2 z = *reinterpret_cast<const float2 *>(&sc->kin[16 * kb + 8 * n + 2 * tc]);
+                    for (int e = 0; e < 4; ++e) {
+                        float x = part ? -X[2 * kb + n][e] : 0.f;
+                        if (part == 0)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x = 0.f;
-#pragma unroll
-                    for (int i = TI - 1; i >= 0; --i) {
-                        const uint32_t v = y[kb][i][2 * n + (e >> 1)];
-                        x += e & 1 ? hi_f(v) : lo_f(v);
+                            for (int i = TI - 1; i >= 0; --i) {
+                                const uint32_t v = y[kb][i][2 * n + (e >> 1)];
+                                x += e & 1 ? hi_f(v) : lo_f(v);
+                            }
+                        w[n][e] = x * (e & 1 ? f.y : f.x);
                     }
-                    u[n][e] = x * (e & 1 ? f.y : f.x);
-                    w[n][e] = X[2 * kb + n][e] * -(e & 1 ? z.y : z.x);
                 }
+                split_a<3>(w[0], w[1], u[kb]);
             }
-            split_a<3>(u[0], u[1], a);
-            split_a<3>(w[0], w[1], d);
+            const uint32_t right = st + (part ? L::kK : L::kQ);
 #pragma unroll
             for (int n = 0; n < NN / 16; ++n) {
-                uint32_t bq[TI][4], bk[TI][4];
+                uint32_t b[2][TI][4];
+                float d[2][4] = {};
 #pragma unroll
-                for (int z = 0; z < TI; ++z) {
-                    ldsm4t(bq[z], addr_bt<NB>(st + L::kQ + z * TB, 16 * kb, 2 * n));
-                    ldsm4t(bk[z], addr_bt<NB>(st + L::kK + z * TB, 16 * kb, 2 * n));
-                }
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int z = 0; z < TI; ++z) ldsm4t(b[kb][z], addr_bt<NB>(right + z * TB, 16 * kb, 2 * n));
 #pragma unroll
                 for (int x = 2; x >= 0; --x)
 #pragma unroll
                     for (int z = TI - 1; z >= 0; --z) {
                         if (x + z > 2) continue;
-                        mma(S[2 * n], a[x], bq[z][0], bq[z][1]);
-                        mma(S[2 * n + 1], a[x], bq[z][2], bq[z][3]);
-                        mma(S[2 * n], d[x], bk[z][0], bk[z][1]);
-                        mma(S[2 * n + 1], d[x], bk[z][2], bk[z][3]);
+#pragma unroll
+                        for (int kb = 0; kb < 2; ++kb) {
+                            mma(d[0], u[kb][x], b[kb][z][0], b[kb][z][1]);
+                            mma(d[1], u[kb][x], b[kb][z][2], b[kb][z][3]);
+                        }
                     }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    S[2 * n][e] = part ? S[2 * n][e] + d[0][e] : fmaf(whole, S[2 * n][e], d[0][e]);
+                    S[2 * n + 1][e] = part ? S[2 * n + 1][e] + d[1][e] : fmaf(whole, S[2 * n + 1][e], d[1][e]);
+                }
             }
         }
         if constexpr (F32) {
@@ -298,7 +305,7 @@ struct GradLayout {
 };
 struct GradScalars {
     float ghi[GC], glo[GC], rk[GC], sq[GC], beta[GC], kin[GC], qin[GC], kout[GC], out[GC];
-    float row[4][GC], tail[4][GC], col[4][GC], dq[4][GC], dk[4][GC];
+    float row[4][GC], tail[4][GC], col[4][GC], diag[GC], dq[4][GC], dk[4][GC];
     float ss[GT / 32];
     float whole;
 };
@@ -331,19 +338,27 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const void *src, long lo
     }
 }
 
-// d[0 .. 2 CT) += a b over the pairs of terms that count: a TA terms of a left operand, b TB terms of
-// right operands of 16 columns each.
+// d[0 .. CT) += a b over the pairs of terms that count: a TA terms of a left operand, b TB terms of right operands
+// of 16 columns each. top: 1 only the leading pair, 0 only the others, -1 all.
 template <int TA, int TB, int CT>
-__device__ __forceinline__ void mma_terms(float (&d)[CT][4], const uint32_t (&a)[TA][4], const uint32_t (&b)[TB][CT / 2][4]) {
+__device__ __forceinline__ void mma_terms(float (&d)[CT][4], const uint32_t (&a)[TA][4], const uint32_t (&b)[TB][CT / 2][4], int top = -1) {
     constexpr int most = (TA > TB ? TA : TB) - 1;
 #pragma unroll
     for (int x = TA - 1; x >= 0; --x)
 #pragma unroll
         for (int z = TB - 1; z >= 0; --z) {
-            if (x + z > most) continue;
+            if (x + z > most || (top >= 0 && top != (x + z == 0))) continue;
 #pragma unroll
             for (int n = 0; n < CT; ++n) mma(d[n], a[x], b[z][n >> 1][2 * (n & 1)], b[z][n >> 1][2 * (n & 1) + 1]);
         }
+}
+
+template <int N>
+__device__ __forceinline__ void add_to(float (&x)[N][4], const float (&y)[N][4]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[n][e] += y[n][e];
 }
 
 __device__ __forceinline__ float quad_sum(float x) {        // over the lanes of one row
@@ -482,36 +497,51 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p) {
                     }
                 }
             }
-            // A, B over the value channels; dY S, dX S, E dS'
+            // A, B over the value channels; dY S, dX S, E dS'. fp32: the slice's sums on their own, small products
+            // first (the tensor cores cut as they add, see Acc), then added to the others.
+            float tA[2][4] = {}, tB[2][4] = {}, tq[CT][4] = {}, tk[CT][4] = {}, to[CT][4] = {};
+            float (&A_)[2][4] = F32 ? tA : A, (&B_)[2][4] = F32 ? tB : B;
+            float (&q_)[CT][4] = F32 ? tq : aq, (&k_)[CT][4] = F32 ? tk : ak, (&o_)[CT][4] = F32 ? to : ao;
+#pragma unroll
+            for (int pass = 0; pass < (F32 ? 2 : 1); ++pass) {
+                const int top = F32 ? pass : -1;
 #pragma unroll 1
-            for (int ks = 0; ks < DW / 16; ++ks) {
-                uint32_t y[TI][4], x[TE][4], e[TE][4];
+                for (int ks = 0; ks < DW / 16; ++ks) {
+                    uint32_t y[TI][4], x[TE][4], e[TE][4];
 #pragma unroll
-                for (int i = 0; i < TI; ++i) ldsm4(y[i], addr_a<YNB>(base + L::kY + i * L::YB, 16 * wr, ks));
+                    for (int i = 0; i < TI; ++i) ldsm4(y[i], addr_a<YNB>(base + L::kY + i * L::YB, 16 * wr, ks));
 #pragma unroll
-                for (int i = 0; i < TE; ++i) {
-                    ldsm4(x[i], addr_a<YNB>(base + L::kX + i * L::YB, 16 * wr, ks));
-                    ldsm4(e[i], addr_a<YNB>(base + L::kE + i * L::YB, 16 * wr, ks));
+                    for (int i = 0; i < TE; ++i) {
+                        ldsm4(x[i], addr_a<YNB>(base + L::kX + i * L::YB, 16 * wr, ks));
+                        ldsm4(e[i], addr_a<YNB>(base + L::kE + i * L::YB, 16 * wr, ks));
+                    }
+                    if (wc <= wr) {         // tokens j of this warp's column group are not all behind its rows
+                        uint32_t b[TE][1][4];
+#pragma unroll
+                        for (int i = 0; i < TE; ++i) ldsm4(b[i][0], addr_b<YNB>(base + L::kE + i * L::YB, j0, ks));
+                        mma_terms<TI, TE, 2>(A_, y, b, top);
+                        mma_terms<TE, TE, 2>(B_, x, b, top);
+                    }
+                    uint32_t b[TE][CT / 2][4];
+#pragma unroll
+                    for (int i = 0; i < TE; ++i)
+#pragma unroll
+                        for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kS + i * L::SB, 16 * ks, c0 / 8 + 2 * m));
+                    mma_terms<TI, TE, CT>(q_, y, b, top);
+                    mma_terms<TE, TE, CT>(k_, x, b, top);
+#pragma unroll
+                    for (int i = 0; i < TE; ++i)
+#pragma unroll
+                        for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kD + i * L::SB, 16 * ks, c0 / 8 + 2 * m));
+                    mma_terms<TE, TE, CT>(o_, e, b, top);
                 }
-                if (wc <= wr) {         // tokens j of this warp's column group are not all behind its rows
-                    uint32_t b[TE][1][4];
-#pragma unroll
-                    for (int i = 0; i < TE; ++i) ldsm4(b[i][0], addr_b<YNB>(base + L::kE + i * L::YB, j0, ks));
-                    mma_terms<TI, TE, 2>(A, y, b);
-                    mma_terms<TE, TE, 2>(B, x, b);
-                }
-                uint32_t b[TE][CT / 2][4];
-#pragma unroll
-                for (int i = 0; i < TE; ++i)
-#pragma unroll
-                    for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kS + i * L::SB, 16 * ks, c0 / 8 + 2 * m));
-                mma_terms<TI, TE, CT>(aq, y, b);
-                mma_terms<TE, TE, CT>(ak, x, b);
-#pragma unroll
-                for (int i = 0; i < TE; ++i)
-#pragma unroll
-                    for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kD + i * L::SB, 16 * ks, c0 / 8 + 2 * m));
-                mma_terms<TE, TE, CT>(ao, e, b);
+            }
+            if constexpr (F32) {
+                add_to(A, tA);
+                add_to(B, tB);
+                add_to(aq, tq);
+                add_to(ak, tk);
+                add_to(ao, to);
             }
             for (int i = tid; i < DW * NN / 2; i += GT) {       // <S, dS'>
                 const float2 a = pair_at<NB, TE>(base + L::kS, L::SB, i / (NN / 2), 2 * (i % (NN / 2)));
@@ -522,18 +552,20 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p) {
         // the keys' and queries' products
         float QK[2][4] = {}, KK[2][4] = {};
         if (wc <= wr) {
-#pragma unroll 1
-            for (int ks = 0; ks < NN / 16; ++ks) {
-                uint32_t a[TI][4], d[TI][4], b[TI][1][4];
 #pragma unroll
-                for (int i = 0; i < TI; ++i) {
-                    ldsm4(a[i], addr_a<NB>(base + L::kQ + i * L::KB, 16 * wr, ks));
-                    ldsm4(d[i], addr_a<NB>(base + L::kK + i * L::KB, 16 * wr, ks));
-                    ldsm4(b[i][0], addr_b<NB>(base + L::kK + i * L::KB, j0, ks));
+            for (int pass = 0; pass < (F32 ? 2 : 1); ++pass)
+#pragma unroll 1
+                for (int ks = 0; ks < NN / 16; ++ks) {
+                    uint32_t a[TI][4], d[TI][4], b[TI][1][4];
+#pragma unroll
+                    for (int i = 0; i < TI; ++i) {
+                        ldsm4(a[i], addr_a<NB>(base + L::kQ + i * L::KB, 16 * wr, ks));
+                        ldsm4(d[i], addr_a<NB>(base + L::kK + i * L::KB, 16 * wr, ks));
+                        ldsm4(b[i][0], addr_b<NB>(base + L::kK + i * L::KB, j0, ks));
+                    }
+                    mma_terms<TI, TI, 2>(QK, a, b, F32 ? pass : -1);
+                    mma_terms<TI, TI, 2>(KK, d, b, F32 ? pass : -1);
                 }
-                mma_terms<TI, TI, 2>(QK, a, b);
-                mma_terms<TI, TI, 2>(KK, d, b);
-            }
         }
         __syncthreads();                // the slice has been read, the scalars are there
         // rows i = 16 wr + gr (+ 8), columns j = j0 + 8 m + 2 tc (+ 1)
@@ -551,8 +583,12 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p) {
                     const float d = fast_exp((sc->ghi[i] - sc->ghi[j + f]) + (sc->glo[i] - sc->glo[j + f])) * sc->rk[j + f];
                     const float nn = j + f <= i ? A[m][e + f] * d * sc->sq[i] : 0.f, oo = j + f < i ? B[m][e + f] * d * sc->rk[i] : 0.f;
                     const float z = nn * QK[m][e + f] - oo * KK[m][e + f], bt = sc->beta[j + f];
-                    cols[f] += z;
-                    rows[e >> 1] = fmaf(bt, z, rows[e >> 1]);
+                    if (j + f == i) {       // z_ii belongs to beta alone: g_i changes neither side of it
+                        sc->diag[i] = z;
+                    } else {
+                        cols[f] += z;
+                        rows[e >> 1] = fmaf(bt, z, rows[e >> 1]);
+                    }
                     vn[f] = nn * bt;
                     vo[f] = -oo * bt;
                 }
@@ -600,67 +636,80 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p) {
         for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         if (lane == 0) sc->ss[warp] = ss;
         __syncthreads();
-        // sq dQ += n K, rk dK -= o K: depth j up to this row block
+        float tQ[CT][4] = {}, tK[CT][4] = {};
+        float (&Q_)[CT][4] = F32 ? tQ : DQ, (&K_)[CT][4] = F32 ? tK : DK;
+#pragma unroll
+        for (int pass = 0; pass < (F32 ? 2 : 1); ++pass) {
+            const int top = F32 ? pass : -1;
+            // sq dQ += n K, rk dK -= o K: depth j up to this row block
 #pragma unroll 1
-        for (int kb = 0; kb <= wr; ++kb) {
-            uint32_t a[TE][4], d[TE][4], b[TI][CT / 2][4];
+            for (int kb = 0; kb <= wr; ++kb) {
+                uint32_t a[TE][4], d[TE][4], b[TI][CT / 2][4];
 #pragma unroll
-            for (int i = 0; i < TE; ++i) {
-                ldsm4(a[i], addr_a<GC * 2>(base + L::kN + i * L::MB, 16 * wr, kb));
-                ldsm4(d[i], addr_a<GC * 2>(base + L::kO + i * L::MB, 16 * wr, kb));
+                for (int i = 0; i < TE; ++i) {
+                    ldsm4(a[i], addr_a<GC * 2>(base + L::kN + i * L::MB, 16 * wr, kb));
+                    ldsm4(d[i], addr_a<GC * 2>(base + L::kO + i * L::MB, 16 * wr, kb));
+                }
+#pragma unroll
+                for (int i = 0; i < TI; ++i)
+#pragma unroll
+                    for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kK + i * L::KB, 16 * kb, c0 / 8 + 2 * m));
+                mma_terms<TE, TI, CT>(Q_, a, b, top);
+                mma_terms<TE, TI, CT>(K_, d, b, top);
             }
+            // rk dK += n^T Q - o^T K: depth i from this row block on
+#pragma unroll 1
+            for (int ib = wr; ib < 4; ++ib) {
+                uint32_t a[TE][4], d[TE][4], b[TI][CT / 2][4];
+                const uint32_t at = tile<GC * 2>(16 * ib + (lane & 7) + ((lane >> 4) << 3), 2 * wr + ((lane >> 3) & 1));
 #pragma unroll
-            for (int i = 0; i < TI; ++i)
+                for (int i = 0; i < TE; ++i) {
+                    ldsm4t(a[i], base + L::kN + i * L::MB + at);
+                    ldsm4t(d[i], base + L::kO + i * L::MB + at);
+                }
 #pragma unroll
-                for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kK + i * L::KB, 16 * kb, c0 / 8 + 2 * m));
-            mma_terms<TE, TI, CT>(DQ, a, b);
-            mma_terms<TE, TI, CT>(DK, d, b);
+                for (int i = 0; i < TI; ++i)
+#pragma unroll
+                    for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kQ + i * L::KB, 16 * ib, c0 / 8 + 2 * m));
+                mma_terms<TE, TI, CT>(K_, a, b, top);
+#pragma unroll
+                for (int i = 0; i < TI; ++i)
+#pragma unroll
+                    for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kK + i * L::KB, 16 * ib, c0 / 8 + 2 * m));
+                mma_terms<TE, TI, CT>(K_, d, b, top);
+            }
         }
-        // rk dK += n^T Q - o^T K: depth i from this row block on
-#pragma unroll 1
-        for (int ib = wr; ib < 4; ++ib) {
-            uint32_t a[TE][4], d[TE][4], b[TI][CT / 2][4];
-            const uint32_t at = tile<GC * 2>(16 * ib + (lane & 7) + ((lane >> 4) << 3), 2 * wr + ((lane >> 3) & 1));
-#pragma unroll
-            for (int i = 0; i < TE; ++i) {
-                ldsm4t(a[i], base + L::kN + i * L::MB + at);
-                ldsm4t(d[i], base + L::kO + i * L::MB + at);
-            }
-#pragma unroll
-            for (int i = 0; i < TI; ++i)
-#pragma unroll
-                for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kQ + i * L::KB, 16 * ib, c0 / 8 + 2 * m));
-            mma_terms<TE, TI, CT>(DK, a, b);
-#pragma unroll
-            for (int i = 0; i < TI; ++i)
-#pragma unroll
-                for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kK + i * L::KB, 16 * ib, c0 / 8 + 2 * m));
-            mma_terms<TE, TI, CT>(DK, d, b);
+        if constexpr (F32) {
+            add_to(DQ, tQ);
+            add_to(DK, tK);
         }
         if (warp == 0) {                // dbeta and dg: two tokens per lane, sums in a fixed order
-            float db[2], dG[2], tail = 0.f, sum = 0.f;
+            float db[2], dG[2], bt[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = 2 * lane + e;
                 const float t = (sc->tail[0][i] + sc->tail[1][i]) + (sc->tail[2][i] + sc->tail[3][i]);
-                db[e] = t + ((sc->col[0][i] + sc->col[1][i]) + (sc->col[2][i] + sc->col[3][i]));
-                dG[e] = ((sc->row[0][i] + sc->row[1][i]) + (sc->row[2][i] + sc->row[3][i])) - sc->beta[i] * db[e];
-                tail = fmaf(sc->beta[i], t, tail);
+                const float c = (sc->col[0][i] + sc->col[1][i]) + (sc->col[2][i] + sc->col[3][i]);
+                db[e] = t + sc->diag[i] + c;
+                dG[e] = ((sc->row[0][i] + sc->row[1][i]) + (sc->row[2][i] + sc->row[3][i])) - sc->beta[i] * c;
+                bt[e] = sc->beta[i] * t;
             }
             float x = lane < GT / 32 ? sc->ss[lane] : 0.f;
 #pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                x += __shfl_xor_sync(0xffffffffu, x, o);
-                tail += __shfl_xor_sync(0xffffffffu, tail, o);
-            }
-            sum = dG[0] + dG[1];
+            for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            // from a token on: what depends on G_i there; before it: what reaches the chunk's end from there
+            float later = dG[0] + dG[1], before = bt[0] + bt[1];
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {      // over this lane's tokens and the later ones
-                const float z = __shfl_down_sync(0xffffffffu, sum, o);
-                if (lane + o < 32) sum += z;
+            for (int o = 1; o < 32; o <<= 1) {
+                const float z = __shfl_down_sync(0xffffffffu, later, o), w = __shfl_up_sync(0xffffffffu, before, o);
+                if (lane + o < 32) later += z;
+                if (lane >= o) before += w;
             }
-            const float last = fmaf(sc->whole, x, tail);
-            const float dg[2] = {sum + last, sum - dG[0] + last};
+            float up = __shfl_up_sync(0xffffffffu, before, 1), down = __shfl_down_sync(0xffffffffu, later, 1);
+            if (lane == 0) up = 0.f;
+            if (lane == 31) down = 0.f;
+            const float last = sc->whole * x;
+            const float dg[2] = {((dG[0] + dG[1]) + down) + (up + last), (dG[1] + down) + ((up + bt[0]) + last)};
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 if (2 * lane + e < n) {

@@ -142,7 +142,8 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
         const Scalars *sc = reinterpret_cast<const Scalars *>(sm + (c % L::stages) * L::stage + L::kS);
         const long long t = t0 + (long long)c * C;
         const int n_tok = int(min((long long)C, t1 - t));
-        float X[4][4] = {}, Y[4][4] = {};
+        Acc<F32, 4> xa, ya, ea;
+        float (&X)[4][4] = xa.d, (&Y)[4][4] = ya.d, (&E)[4][4] = ea.d;
         [[maybe_unused]] float V[4][4];
         [[maybe_unused]] uint32_t vraw[2][4];
         if constexpr (F32) {    // loaded under the products
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
                 for (int z = TI - 1; z >= 0; --z) {
                     if (x + z > 2) continue;
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) mma(X[n], a[x], b[z][n >> 1][2 * (n & 1)], b[z][n >> 1][2 * (n & 1) + 1]);
+                    for (int n = 0; n < 4; ++n) xa.add(n, x + z == 0, a[x], b[z][n >> 1][2 * (n & 1)], b[z][n >> 1][2 * (n & 1) + 1]);
                 }
             if constexpr (!STATES) {
 #pragma unroll
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
                     for (int z = TI - 1; z >= 0; --z) {
                         if (x + z > TS - 1) continue;
 #pragma unroll
-                        for (int n = 0; n < 4; ++n) mma(Y[n], a[x], b[z][n >> 1][2 * (n & 1)], b[z][n >> 1][2 * (n & 1) + 1]);
+                        for (int n = 0; n < 4; ++n) ya.add(n, x + z == 0, a[x], b[z][n >> 1][2 * (n & 1)], b[z][n >> 1][2 * (n & 1) + 1]);
                     }
             }
         }
@@ -221,6 +222,8 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
                 V[n][3] = hi_f(vraw[n >> 1][2 * (n & 1) + 1]);
             }
         }
+        xa.join();
+        ya.join();
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const float2 in = *reinterpret_cast<const float2 *>(&sc->kin[8 * n + 2 * tc]);
@@ -235,7 +238,6 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
         uint32_t bad = 0;
         if (careful) take_out(X, bad);
         // E^T = X^T W^T
-        float E[4][4] = {};
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             uint32_t a[3][4];
@@ -249,11 +251,12 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
                 for (int x = 2; x >= 0; --x)
 #pragma unroll
                     for (int z = 2 - x; z >= 0; --z) {
-                        mma(E[2 * ib], a[x], w[z][0], w[z][1]);
-                        mma(E[2 * ib + 1], a[x], w[z][2], w[z][3]);
+                        ea.add(2 * ib, x + z == 0, a[x], w[z][0], w[z][1]);
+                        ea.add(2 * ib + 1, x + z == 0, a[x], w[z][2], w[z][3]);
                     }
             }
         }
+        ea.join();
         if (careful) take_out(E, bad);
         if constexpr (STATES) {
 #pragma unroll
@@ -276,40 +279,46 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
 #pragma unroll
                     for (int z = TP - 1; z >= 0; --z) {
                         if (x + z > TS - 1) continue;
-                        mma(Y[2 * ib], a[x], w[z][0], w[z][1]);
-                        mma(Y[2 * ib + 1], a[x], w[z][2], w[z][3]);
+                        ya.add(2 * ib, x + z == 0, a[x], w[z][0], w[z][1]);
+                        ya.add(2 * ib + 1, x + z == 0, a[x], w[z][2], w[z][3]);
                     }
             }
         }
-        // S <- exp(G_C) S + U^T K, U = out E
+        ya.join();
+        // S <- exp(G_C) S + U^T K, U = out E: what is added is summed on its own, small products first
         const float whole = sc->whole;
+        uint32_t u[2][3][4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const float2 o = *reinterpret_cast<const float2 *>(&sc->out[8 * n + 2 * tc]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) E[n][e] *= e & 1 ? o.y : o.x;
         }
+        split_a<3>(E[0], E[1], u[0]);
+        split_a<3>(E[2], E[3], u[1]);
 #pragma unroll
-        for (int n = 0; n < NN / 8; ++n)
+        for (int n = 0; n < NN / 16; ++n) {
+            uint32_t b[2][TI][4];
+            float d[2][4] = {};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) S[n][e] *= whole;
+            for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            uint32_t a[3][4];
-            split_a<3>(E[2 * kb], E[2 * kb + 1], a);
+                for (int z = 0; z < TI; ++z) ldsm4t(b[kb][z], addr_bt<NB>(st + L::kK + z * TB, 16 * kb, 2 * n));
 #pragma unroll
-            for (int n = 0; n < NN / 16; ++n) {
-                uint32_t b[TI][4];
+            for (int x = 2; x >= 0; --x)
 #pragma unroll
-                for (int z = 0; z < TI; ++z) ldsm4t(b[z], addr_bt<NB>(st + L::kK + z * TB, 16 * kb, 2 * n));
+                for (int z = TI - 1; z >= 0; --z) {
+                    if (x + z > 2) continue;
 #pragma unroll
-                for (int x = 2; x >= 0; --x)
-#pragma unroll
-                    for (int z = TI - 1; z >= 0; --z) {
-                        if (x + z > 2) continue;
-                        mma(S[2 * n], a[x], b[z][0], b[z][1]);
-                        mma(S[2 * n + 1], a[x], b[z][2], b[z][3]);
+                    for (int kb = 0; kb < 2; ++kb) {
+                        mma(d[0], u[kb][x], b[kb][z][0], b[kb][z][1]);
+                        mma(d[1], u[kb][x], b[kb][z][2], b[kb][z][3]);
                     }
+                }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                S[2 * n][e] = fmaf(whole, S[2 * n][e], d[0][e]);
+                S[2 * n + 1][e] = fmaf(whole, S[2 * n + 1][e], d[1][e]);
             }
         }
         if (careful) {

@@ -97,6 +97,38 @@ __device__ __forceinline__ void split_a(const float (&u)[4], const float (&v)[4]
         for (int j = 0; j < 4; ++j) a[i][j] = r[j][i];
 }
 
+// The tensor cores cut, not round, as they add to an accumulator (half a unit in the last place each time, always
+// towards zero). Where fp32's accuracy is wanted the products of leading terms therefore get an
+// accumulator of their own, so that it sees few additions, and the small products another.
+template <bool TWO, int N>
+struct Acc {
+    float d[N][4], small[TWO ? N : 1][4];
+    __device__ __forceinline__ Acc() {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                d[n][e] = 0.f;
+                if (TWO) small[n % (TWO ? N : 1)][e] = 0.f;
+            }
+    }
+    __device__ __forceinline__ void add(int n, bool leading, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        if (TWO && !leading) mma(small[TWO ? n : 0], a, b0, b1);
+        else mma(d[n], a, b0, b1);
+    }
+    __device__ __forceinline__ void join() {
+        if constexpr (TWO) {
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    d[n][e] += small[n][e];
+                    small[n][e] = 0.f;
+                }
+        }
+    }
+};
+
 // Byte offset of 16-byte chunk c of row r in a tile of rows of NB bytes (64 or a multiple of 128): eight rows
 // of one chunk column lie in eight different bank groups.
 template <int NB> __device__ __forceinline__ uint32_t tile(int r, int c) {
@@ -236,7 +268,8 @@ __device__ __forceinline__ void prepare_chunk(uint32_t k, uint32_t q, unsigned c
     const uint32_t left = queries ? q : k, w_out = smem_addr(w_at);
     float *scratch = reinterpret_cast<float *>(w_at);
     // products with the keys, tiles (m, n): (0, 0), (0, 1), (1, 0), (1, 1), (1, 2), (1, 3)
-    float acc[6][4] = {};
+    Acc<(TI > 1), 6> prod;
+    float (&acc)[6][4] = prod.d;
     float len[4] = {};
     if (TP > 0 || !queries) {
 #pragma unroll 1
@@ -253,12 +286,13 @@ __device__ __forceinline__ void prepare_chunk(uint32_t k, uint32_t q, unsigned c
         for (int x = TI - 1; x >= 0; --x)
 #pragma unroll
             for (int y = TI - 1 - x; y >= 0; --y) {
-                mma(acc[0], a0[x], b0[y][0], b0[y][1]);
-                mma(acc[1], a0[x], b0[y][2], b0[y][3]);
-                mma(acc[2], a1[x], b0[y][0], b0[y][1]);
-                mma(acc[3], a1[x], b0[y][2], b0[y][3]);
-                mma(acc[4], a1[x], b1[y][0], b1[y][1]);
-                mma(acc[5], a1[x], b1[y][2], b1[y][3]);
+                const bool top = x + y == 0;
+                prod.add(0, top, a0[x], b0[y][0], b0[y][1]);
+                prod.add(1, top, a0[x], b0[y][2], b0[y][3]);
+                prod.add(2, top, a1[x], b0[y][0], b0[y][1]);
+                prod.add(3, top, a1[x], b0[y][2], b0[y][3]);
+                prod.add(4, top, a1[x], b1[y][0], b1[y][1]);
+                prod.add(5, top, a1[x], b1[y][2], b1[y][3]);
             }
         // the rows' squares from the same fragments: rows gr, gr + 8, 16 + gr, 24 + gr
 #pragma unroll
@@ -281,6 +315,7 @@ __device__ __forceinline__ void prepare_chunk(uint32_t k, uint32_t q, unsigned c
         len[r] += __shfl_xor_sync(0xffffffffu, len[r], 2);
     }
     }
+    prod.join();
     if (!queries) {
         const bool fine = len[0] + len[1] + len[2] + len[3] < INFINITY && g <= 80.f && fabsf(beta) < INFINITY;
         const bool odd = __any_sync(0xffffffffu, !fine);
