@@ -1,19 +1,21 @@
 // Beam search over recurrent states: the selection of the best continuations over beams and
 // vocabulary, and the reordering of the states' rows.
 //
-// Selection reads the logits once. beam_part_kernel: a CTA takes a segment of one row into registers,
-// sums its exponentials against its own maximum, and finds its M best elements as 64-bit keys
-// (order-preserving bits of the value above the complement of the index, so that keys never tie and
-// equal values go to the lowest index). The M-th largest of the 256 threads' own maxima is a floor
-// for the M-th best element, and only the M threads at or above it can hold more, so the elements that
-// pass the floor fit a buffer of M times a thread's elements whatever the input. beam_pick_kernel: one
-// CTA per request joins the segments' sums in fp64, merges the sorted lists of a row and then those
-// of the rows. An element's place in a merged list is its place in its own plus, for every other list,
-// how many there precede it (a binary search), so nothing is sorted twice. Bound by the logits' bytes
-// where the batch is large, by two launches where it is small.
+// Selection reads the logits once. beam_part_kernel: a CTA takes a segment of one row into registers (packed, as
+// loaded), sums its exponentials against its own maximum, and finds its M best elements. The M-th
+// largest of the 256 threads' own maxima is a floor for the M-th best element: M elements at least reach
+// it, and those above it lie in fewer than M threads. What reaches the floor is gathered and placed by
+// counting; only where more elements equal the floor than there is room for are they taken in the
+// order of their index instead. The lists hold 64-bit keys, order-preserving bits of the value above the
+// complement of the index, so that keys never tie and equal values go to the lowest index.
+// beam_pick_kernel: one CTA per request joins the segments' sums in fp64, merges the sorted lists of a row and
+// then those of the rows. An element's place in a merged list is its place in its own plus, for every
+// other list, how many there precede it (a binary search), so nothing is sorted twice.
 #include "beam.cuh"
 
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 namespace wkv7 {
 namespace {
@@ -41,9 +43,6 @@ __device__ __forceinline__ unsigned long long make_key(float x, uint32_t index) 
     const uint32_t o = order_bits(x == 0.f ? 0.f : x);   // -0 and +0 are the same score
     return o ? ((unsigned long long)o << 32) | (0xffffffffu - index) : 0ull;
 }
-
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 // 16 bytes from p, which lies `shift` elements behind a 16-byte boundary: the two aligned vectors
 // around it, shifted together. Rows of an odd vocabulary start anywhere; equal rows must be cut into
@@ -81,22 +80,88 @@ __device__ __forceinline__ void unpack(const uint4 v, float (&x)[8]) {
     }
 }
 
-// Sorts one key per lane over the warp, largest in lane 0.
-__device__ __forceinline__ unsigned long long warp_sort_desc(unsigned long long k) {
+// The elements from i on of a row that ends before a whole vector does; -inf behind its end.
+__device__ __forceinline__ uint4 load_edge(const float *p, int i, int n) {
+    float t[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] = i + e < n ? p[i + e] : -INFINITY;
+    return make_uint4(__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]), __float_as_uint(t[3]));
+}
+__device__ __forceinline__ uint4 load_edge(const __nv_bfloat16 *p, int i, int n) {
+    const unsigned short *u = reinterpret_cast<const unsigned short *>(p);
+    uint32_t t[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = i + e < n ? u[i + e] : 0xff80u;
+    return make_uint4(t[0] | t[1] << 16, t[2] | t[3] << 16, t[4] | t[5] << 16, t[6] | t[7] << 16);
+}
+
+// The thread's largest element (NaN only if all are).
+template <int NV>
+__device__ __forceinline__ float largest(const uint4 (&v)[NV], const float *) {
+    float m = __uint_as_float(v[0].x);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        float x[4];
+        unpack(v[j], x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = fmaxf(m, x[e]);
+    }
+    return m;
+}
+template <int NV>
+__device__ __forceinline__ float largest(const uint4 (&v)[NV], const __nv_bfloat16 *) {
+    auto b2 = [](const uint32_t &u) { return *reinterpret_cast<const __nv_bfloat162 *>(&u); };
+    __nv_bfloat162 m = b2(v[0].x);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) m = __hmax2(__hmax2(__hmax2(m, b2(v[j].x)), b2(v[j].y)), __hmax2(b2(v[j].z), b2(v[j].w)));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+// Calls f(value, place in the vector) for the elements of a vector that are at least `least`.
+template <class F>
+__device__ __forceinline__ void for_at_least(const uint4 &v, float least, const float *, F f) {
+    float x[4];
+    unpack(v, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (x[e] >= least) f(x[e], e);
+}
+template <class F>
+__device__ __forceinline__ void for_at_least(const uint4 &v, float least, const __nv_bfloat16 *, F f) {
+    const __nv_bfloat162 l = __float2bfloat162_rn(least);      // a logit: exact
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t hit = __hge2_mask(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]), l);
+        if (hit) {
+            if (hit & 0xffffu) f(__uint_as_float(w[i] << 16), 2 * i);
+            if (hit >> 16) f(__uint_as_float(w[i] & 0xffff0000u), 2 * i + 1);
+        }
+    }
+}
+
+// Sorts one value per lane over the warp, largest in lane 0.
+__device__ __forceinline__ uint32_t warp_sort_desc(uint32_t k) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int size = 2; size <= 32; size <<= 1)
 #pragma unroll
         for (int stride = size >> 1; stride; stride >>= 1) {
-            const unsigned long long o = __shfl_xor_sync(0xffffffffu, k, stride);
-            const bool keep_max = ((lane & stride) == 0) == ((lane & size) == 0);
-            k = (keep_max == (o > k)) ? o : k;
+            const uint32_t o = __shfl_xor_sync(0xffffffffu, k, stride);
+            k = ((lane & stride) == 0) == ((lane & size) == 0) ? max(k, o) : min(k, o);
         }
     return k;
 }
 
+// exp in three instructions, relative error about 1e-7 + 6e-8 |x| (a tiny result may become 0).
+__device__ __forceinline__ float quick_exp(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    return y;
+}
+
 // How many of the n keys, sorted from the largest down, are above x.
-__device__ __forceinline__ int count_above(const unsigned long long *list, int n, unsigned long long x) {
+template <class U>
+__device__ __forceinline__ int count_above(const U *list, int n, U x) {
     int lo = 0, hi = n;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -106,86 +171,151 @@ __device__ __forceinline__ int count_above(const unsigned long long *list, int n
     return lo;
 }
 
-template <class Tin, int EPT>
-__global__ void __launch_bounds__(kT) beam_part_kernel(const BeamArgs p, int splits) {
-    constexpr int VW = 16 / sizeof(Tin), NV = EPT / VW, SEG = kT * EPT;
-    extern __shared__ unsigned long long cand[];          // [M * EPT]
-    __shared__ unsigned long long s_sort[kT / 32][32], s_floor;
-    __shared__ float s_top[kT / 32];
-    __shared__ double s_sum[kT / 32];
-    __shared__ int s_n;
+template <class Tin, int NV>
+__global__ void __launch_bounds__(kT, 6) beam_part_kernel(const BeamArgs p, int splits) {
+    constexpr int VW = 16 / sizeof(Tin), EPT = NV * VW, SEG = kT * EPT, W = kT / 32;
+    extern __shared__ unsigned long long cand[];          // [M * EPT + M]
+    __shared__ uint32_t s_sort[W][32], s_floor;
+    __shared__ double s_sum[W];
+    __shared__ int s_n, s_ties[W];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");     // the picking kernel may take its place
     const int row = blockIdx.x / unsigned(splits), split = blockIdx.x % unsigned(splits);
     if (p.finished && p.finished[row]) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Tin *base = static_cast<const Tin *>(p.logits) + (long long)row * p.row_stride;
     const int shift = int((reinterpret_cast<uintptr_t>(base) / sizeof(Tin)) % VW);
-    const int beyond = shift ? VW - shift : 0;            // elements that a shifted load reads behind its own
-    const long long at = (long long)split * SEG + (long long)tid * VW;
-    float x[EPT];
+    const int most = p.V - VW - (shift ? VW - shift : 0);  // last place from which a whole (shifted) vector may be read
+    const int at = split * SEG + tid * VW;                 // V + 65536 fits an int
+    uint4 v[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const long long i = at + (long long)j * kT * VW;
-        float t[VW];
-        if (i + VW + beyond <= p.V) {
-            unpack(load_shifted(base + i, shift), t);
-        } else {
-#pragma unroll
-            for (int e = 0; e < VW; ++e) t[e] = i + e < p.V ? to_f(base[i + e]) : -INFINITY;
-        }
-#pragma unroll
-        for (int e = 0; e < VW; ++e) x[j * VW + e] = t[e];
+        const int i = at + j * kT * VW;
+        if (i <= most) v[j] = load_shifted(base + i, shift);
+        else v[j] = load_edge(base, i, p.V);
     }
     if (tid == 0) {
-        s_floor = 1;
+        s_floor = 0;
         s_n = 0;
     }
-    // the thread's largest element, first of equals (NaN fails every comparison)
-    float top = -INFINITY;
-    int arg = 0;
-#pragma unroll
-    for (int e = 0; e < EPT; ++e)
-        if (x[e] > top) {
-            top = x[e];
-            arg = e;
-        }
-    const uint32_t first = uint32_t(at + (long long)(arg / VW) * kT * VW + arg % VW);
-    const unsigned long long mine = make_key(top, first);
-    const unsigned long long sorted = warp_sort_desc(mine);
+    const float top = largest<NV>(v, static_cast<const Tin *>(nullptr));
+    uint32_t sorted = warp_sort_desc(order_bits(top == 0.f ? 0.f : top));
     s_sort[warp][lane] = sorted;
-    float wtop = top;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) wtop = fmaxf(wtop, __shfl_xor_sync(0xffffffffu, wtop, o));
-    if (lane == 0) s_top[warp] = wtop;
     __syncthreads();
-    float ctop = s_top[0];
+    uint32_t peak = 0;
 #pragma unroll
-    for (int w = 1; w < kT / 32; ++w) ctop = fmaxf(ctop, s_top[w]);
-    // the M-th largest of the threads' maxima
-    if (lane < p.M && sorted) {
-        int rank = lane;
-#pragma unroll
-        for (int w = 0; w < kT / 32; ++w)
-            if (w != warp) rank += count_above(s_sort[w], 32, sorted);
-        if (rank == p.M - 1) s_floor = sorted;
-    }
+    for (int w = 0; w < W; ++w) peak = max(peak, s_sort[w][0]);
+    const float ctop = peak ? order_value(peak) : -INFINITY, ref = peak ? ctop : 0.f;
     float sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) sum += x[e] > -INFINITY ? __expf(x[e] - ctop) : 0.f;
+    for (int j = 0; j < NV; ++j) {
+        float x[VW];
+        unpack(v[j], x);
+#pragma unroll
+        for (int e = 0; e < VW; ++e) sum += quick_exp(x[e] - ref);
+    }
+    if (sum != sum) {                                      // a NaN among them counts as -inf
+        sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float x[VW];
+            unpack(v[j], x);
+#pragma unroll
+            for (int e = 0; e < VW; ++e) sum += quick_exp(fmaxf(x[e], -INFINITY) - ref);
+        }
+    }
     double ds = sum;
 #pragma unroll
     for (int o = 16; o; o >>= 1) ds += __shfl_xor_sync(0xffffffffu, ds, o);
     if (lane == 0) s_sum[warp] = ds;
-    __syncthreads();
-    const unsigned long long low = s_floor;
-    if (mine >= low) {
+    // the M-th largest of the threads' maxima (0: fewer than M threads hold anything): up to 32, by merging the
+    // sorted warps pairwise; above, by counting in the other warps' lists
+    if (p.M <= 32) {
 #pragma unroll
-        for (int e = 0; e < EPT; ++e) {
-            const unsigned long long key = make_key(x[e], uint32_t(at + (long long)(e / VW) * kT * VW + e % VW));
-            if (key >= low) cand[atomicAdd(&s_n, 1)] = key;
+        for (int step = 1; step < W; step *= 2) {
+            __syncthreads();
+            if (warp % (2 * step) == 0) {
+                sorted = max(sorted, s_sort[warp + step][31 - lane]);      // the 32 largest of both, rising then falling
+#pragma unroll
+                for (int stride = 16; stride; stride >>= 1) {
+                    const uint32_t o = __shfl_xor_sync(0xffffffffu, sorted, stride);
+                    sorted = (lane & stride) == 0 ? max(sorted, o) : min(sorted, o);
+                }
+                s_sort[warp][lane] = sorted;
+            }
         }
+        if (warp == 0 && lane == p.M - 1) s_floor = sorted;
+    } else if (sorted) {
+        int above = lane, same = 0;                        // equal values: those of lower warps come first
+        for (int w = 0; w < W; ++w)
+            if (w != warp) {
+                const int a = count_above(s_sort[w], 32, sorted);
+                above += a;
+                if (w < warp) same += count_above(s_sort[w], 32, sorted - 1) - a;
+            }
+        if (above + same == p.M - 1) s_floor = sorted;
     }
     __syncthreads();
-    const int n = s_n;
+    const uint32_t low = s_floor;
+    const float least = low ? order_value(low) : -INFINITY;
+    const int room = p.M * EPT;
+    if (top >= least) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            for_at_least(v[j], least, static_cast<const Tin *>(nullptr), [&](float x, int e) {
+                const unsigned long long key = make_key(x, uint32_t(at + j * kT * VW + e));
+                if (key) {
+                    const int to = atomicAdd(&s_n, 1);
+                    if (to < room) cand[to] = key;
+                }
+            });
+    }
+    __syncthreads();
+    int n = s_n;
+    if (n > room) {             // more elements equal the floor than there is room for: the lowest indices of them
+        __syncthreads();
+        if (tid == 0) s_n = 0;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            for_at_least(v[j], least, static_cast<const Tin *>(nullptr), [&](float x, int e) {
+                if (x > least) cand[atomicAdd(&s_n, 1)] = make_key(x, uint32_t(at + j * kT * VW + e));
+            });
+        __syncthreads();
+        n = s_n;                                           // in fewer than M threads
+        const int need = p.M - min(n, p.M);
+        int got = 0;
+#pragma unroll 1
+        for (int j = 0; j < NV && got < need; ++j) {
+            uint4 u = v[0];
+#pragma unroll
+            for (int i = 1; i < NV; ++i) u = i == j ? v[i] : u;
+            int mine = 0;
+            for_at_least(u, least, static_cast<const Tin *>(nullptr), [&](float x, int) { mine += x == least; });
+            int before = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, before, o);
+                if (lane >= o) before += x;
+            }
+            if (lane == 31) s_ties[warp] = before;
+            __syncthreads();
+            int all = 0;
+            for (int w = 0; w < W; ++w) {
+                if (w < warp) before += s_ties[w];
+                all += s_ties[w];
+            }
+            int to = got + before - mine;
+            for_at_least(u, least, static_cast<const Tin *>(nullptr), [&](float x, int e) {
+                if (x == least) {
+                    if (to < need) cand[n + to] = make_key(x, uint32_t(at + j * kT * VW + e));
+                    ++to;
+                }
+            });
+            got += all;
+            __syncthreads();
+        }
+        n += min(got, need);
+    }
     Part *part = static_cast<Part *>(p.ws);
     unsigned long long *list = reinterpret_cast<unsigned long long *>(part + size_t(p.B) * p.K * splits) +
                                size_t(blockIdx.x) * p.M;
@@ -199,12 +329,13 @@ __global__ void __launch_bounds__(kT) beam_part_kernel(const BeamArgs p, int spl
     if (tid == 0) {
         double t = 0.;
 #pragma unroll
-        for (int w = 0; w < kT / 32; ++w) t += s_sum[w];
-        part[blockIdx.x] = Part{ctop, 0.f, t};
+        for (int w = 0; w < W; ++w) t += s_sum[w];
+        part[blockIdx.x] = Part{ctop, 0.f, peak ? t : 0.};
     }
 }
 
-__global__ void __launch_bounds__(kPickT) beam_pick_kernel(const BeamArgs p, int splits) {
+// staged: the segments' lists fit shared memory behind the rows' results.
+__global__ void __launch_bounds__(kPickT) beam_pick_kernel(const BeamArgs p, int splits, bool staged) {
     extern __shared__ unsigned long long dyn[];
     __shared__ double s_norm[WKV7_BEAM_MAX];
     __shared__ int s_have[WKV7_BEAM_MAX];
@@ -217,6 +348,13 @@ __global__ void __launch_bounds__(kPickT) beam_pick_kernel(const BeamArgs p, int
                                           static_cast<const Part *>(p.ws) + size_t(p.B) * K * splits) +
                                       size_t(b) * K * splits * M;
     for (int i = tid; i < K * M; i += kPickT) best[i] = 0;
+    if (tid < K) s_have[tid] = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");               // the segments are there
+    if (staged) {
+        unsigned long long *to = dyn + 2 * size_t(K) * M;
+        for (int i = tid; i < K * splits * M; i += kPickT) to[i] = lists[i];
+        lists = to;
+    }
     // the rows' normalisers
     for (int j = warp; j < K; j += kPickT / 32) {
         if (p.finished && p.finished[size_t(b) * K + j]) continue;
@@ -237,14 +375,14 @@ __global__ void __launch_bounds__(kPickT) beam_pick_kernel(const BeamArgs p, int
     // each row's M best of its segments' lists
     const int per_row = splits * M;
     for (int i = tid; i < K * per_row; i += kPickT) {
-        const int j = i / per_row, r = i % per_row, s = r / M, pos = r % M;
+        const int j = i / per_row, r = i - j * per_row, s = r / M;
         if (p.finished && p.finished[size_t(b) * K + j]) continue;
         const unsigned long long *row = lists + size_t(j) * per_row;
         const unsigned long long key = row[r];
         if (!key) continue;
-        int rank = pos;
+        int rank = r - s * M;
         for (int o = 0; o < splits && rank < M; ++o)
-            if (o != s) rank += count_above(row + o * M, M, key);
+            if (o != s && row[o * M] > key) rank += count_above(row + o * M, M, key);
         if (rank < M) best[j * M + rank] = key;
     }
     __syncthreads();
@@ -262,7 +400,6 @@ __global__ void __launch_bounds__(kPickT) beam_pick_kernel(const BeamArgs p, int
         }
         score[i] = x > -INFINITY ? x : -INFINITY;          // NaN offers nothing
     }
-    if (tid < K) s_have[tid] = 0;
     __syncthreads();
     for (int i = tid; i < K * M; i += kPickT)              // the valid ones are a prefix of the row
         if (score[i] > -INFINITY && (i % M == M - 1 || !(score[i + 1] > -INFINITY))) s_have[i / M] = i % M + 1;
@@ -341,22 +478,21 @@ cudaError_t reorder_t(int L, int B, int K, size_t row_bytes, const int *parents,
 
 // ---- host side ---------------------------------------------------------------------------------------
 
-// Elements per thread of beam_part_kernel: 32, or 8 where 32 would leave SMs without a segment.
-int elements_per_thread(int B, int K, int V) {
-    return (long long)B * K * ((V - 1) / (kT * 32) + 1) < 2 * 148 ? 8 : 32;
+// Elements per thread of beam_part_kernel: four vectors of 16 bytes (32 bf16, 16 fp32), or 8 elements where
+// that would leave SMs without a segment.
+int elements_per_thread(int B, int K, int V, int whole) {
+    return (long long)B * K * ((V - 1) / (kT * whole) + 1) < 2 * 148 ? 8 : whole;
 }
-int segments(int B, int K, int V) {
-    const int seg = kT * elements_per_thread(B, K, V);
-    return (V - 1) / seg + 1;
-}
+int segments(int B, int K, int V, int whole) { return (V - 1) / (kT * elements_per_thread(B, K, V, whole)) + 1; }
+int whole_of(wkv7_dtype dt) { return dt == WKV7_BF16 ? 32 : 16; }
 
 template <class Tin>
 cudaError_t select_t(const BeamArgs &p) {
-    const int splits = segments(p.B, p.K, p.V), ept = elements_per_thread(p.B, p.K, p.V);
+    const int whole = whole_of(p.dt), splits = segments(p.B, p.K, p.V, whole), ept = elements_per_thread(p.B, p.K, p.V, whole);
     const unsigned grid = unsigned(p.B) * unsigned(p.K) * unsigned(splits);
-    const size_t smem = size_t(p.M) * ept * 8;            // at most 16 KB
-    if (ept == 8) beam_part_kernel<Tin, 8><<<grid, kT, smem, p.stream>>>(p, splits);
-    else beam_part_kernel<Tin, 32><<<grid, kT, smem, p.stream>>>(p, splits);
+    const size_t smem = size_t(p.M) * (ept + 1) * 8;      // at most 16.5 KB
+    if (ept == 8) beam_part_kernel<Tin, sizeof(Tin) / 2><<<grid, kT, smem, p.stream>>>(p, splits);
+    else beam_part_kernel<Tin, 4><<<grid, kT, smem, p.stream>>>(p, splits);
     return cudaGetLastError();
 }
 
@@ -365,17 +501,31 @@ cudaError_t select_t(const BeamArgs &p) {
 cudaError_t allow_dynamic_smem(const void *kernel, int bytes);
 
 size_t beam_select_workspace(int B, int K, int V, int M) {
-    return size_t(B) * K * segments(B, K, V) * (sizeof(Part) + size_t(M) * 8);
+    const int n = std::max(segments(B, K, V, 16), segments(B, K, V, 32));     // either type's
+    return size_t(B) * K * size_t(n) * (sizeof(Part) + size_t(M) * 8);
 }
 
 cudaError_t launch_beam_select(const BeamArgs &p) {
-    const int smem = p.K * p.M * 16;                      // at most 64 KB
-    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(beam_pick_kernel), WKV7_BEAM_MAX * WKV7_BEAM_MAX * 16);
+    constexpr int most = 160 * 1024;
+    const int splits = segments(p.B, p.K, p.V, whole_of(p.dt));
+    const size_t rows = size_t(p.K) * p.M * 16, lists = size_t(p.K) * splits * p.M * 8;     // rows: at most 64 KB
+    const bool staged = rows + lists <= most;
+    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(beam_pick_kernel), most);
     if (e != cudaSuccess) return e;
     e = p.dt == WKV7_BF16 ? select_t<__nv_bfloat16>(p) : select_t<float>(p);
     if (e != cudaSuccess) return e;
-    beam_pick_kernel<<<p.B, kPickT, smem, p.stream>>>(p, segments(p.B, p.K, p.V));
-    return cudaGetLastError();
+    // launched while the segments still run: its blocks start as theirs end, and wait for the last of them
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(unsigned(p.B));
+    c.blockDim = dim3(kPickT);
+    c.dynamicSmemBytes = rows + (staged ? lists : 0);
+    c.stream = p.stream;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, beam_pick_kernel, p, splits, staged);
 }
 
 cudaError_t launch_beam_reorder(int L, int B, int K, size_t row_bytes, const int *parents, const void *src, void *dst,

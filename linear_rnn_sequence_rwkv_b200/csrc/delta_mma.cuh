@@ -242,8 +242,12 @@ template <bool F32> struct Gate {
 };
 
 // exp for decays between tokens: two instructions, relative error about 1e-7 + 6e-8 |x|, so the decays
-// that weigh anything keep fp32's accuracy.
-__device__ __forceinline__ float fast_exp(float x) { return __expf(x); }
+// that weigh anything keep fp32's accuracy (denormal results become 0).
+__device__ __forceinline__ float fast_exp(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    return y;
+}
 
 // The state-free part of one chunk, by a group of two warps (`queries`: this warp's role; named barrier
 // `bar`). With D_ij = exp(G_i - G_j) and unit or given q, k:

@@ -11,7 +11,6 @@ outputs are copied back (the end-to-end path).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -83,6 +82,8 @@ def library_path() -> str:
 def load():
     """Load libwkv7.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -634,50 +635,71 @@ def forward_host(r, w, k, v, kk, a, S0, y, S_T, workspace, *, algo="auto", chunk
 # ---- gated delta rule, beam search -----------------------------------------------------------------
 
 
-@contextlib.contextmanager
-def _on(dev, stream):
+class _On:
     """The tensors' device, and `stream` as the current one where the caller names it: what is
-    allocated inside belongs to the stream that the kernels run on."""
-    with torch.cuda.device(dev):
-        if stream is None:
-            yield ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
-        else:
-            with torch.cuda.stream(stream):
-                yield ctypes.c_void_p(stream.cuda_stream)
+    allocated inside belongs to the stream that the kernels run on. Entering gives the stream's handle;
+    the usual case, the current stream of the current device, changes nothing."""
+    __slots__ = ("dev", "stream", "held")
+
+    def __init__(self, dev, stream):
+        if dev.type != "cuda":
+            raise ValueError(f"the tensors are on {dev}: this function takes CUDA tensors")
+        self.dev, self.stream, self.held = dev, stream, None
+
+    def __enter__(self):
+        if self.stream is not None:
+            self.held = (torch.cuda.device(self.dev), torch.cuda.stream(self.stream))
+        elif self.dev.index != torch._C._cuda_getDevice():
+            self.held = (torch.cuda.device(self.dev),)
+        if self.held is None:
+            return torch._C._cuda_getCurrentRawStream(self.dev.index)
+        for c in self.held:
+            c.__enter__()
+        return torch.cuda.current_stream(self.dev).cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.held or ()):
+            c.__exit__(*exc)
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _wrong(name, t, shape, dtype, dev):
+    """Raises what is wrong with a tensor that is not of this shape, type and device."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _plain(name, t, shape, dtype, dev):
     """A dense tensor of this shape, type and device, or an error that names it."""
-    _need(tuple(t.shape) == tuple(shape), f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-    _need(t.device == dev, f"{name} is on {t.device}, expected {dev}")
-    _need(t.is_contiguous(), f"{name} must be contiguous")
+    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        _wrong(name, t, shape, dtype, dev)
 
 
 def _row_stride(name, t, shape, dtype, dev):
     """Elements from one token's row to the next of a tensor whose heads and channels are dense and
     whose rows are evenly spaced over all leading dimensions (0 for the dense layout)."""
-    _need(tuple(t.shape) == tuple(shape), f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-    _need(t.device == dev, f"{name} is on {t.device}, expected {dev}")
+    if t.shape != shape or t.dtype != dtype or t.device != dev:
+        _wrong(name, t, shape, dtype, dev)
     if t.is_contiguous():
         return 0
-    _need((t.shape[-1] == 1 or t.stride(-1) == 1) and (t.shape[-2] == 1 or t.stride(-2) == t.shape[-1]),
-          f"{name} must be dense over its heads and channels")
+    if not ((t.shape[-1] == 1 or t.stride(-1) == 1) and (t.shape[-2] == 1 or t.stride(-2) == t.shape[-1])):
+        raise ValueError(f"{name} must be dense over its heads and channels")
     row, step = None, 0
     for n, st in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
         if n == 1:
             continue
         if row is None:
             row, step = st, st
-        _need(st == step, f"{name}: its rows are not evenly spaced; make it contiguous")
+        if st != step:
+            raise ValueError(f"{name}: its rows are not evenly spaced; make it contiguous")
         step *= n
     return 0 if row is None else row
 
@@ -685,23 +707,25 @@ def _row_stride(name, t, shape, dtype, dev):
 def _delta_args(q, k, v, g, beta, scale, qk_norm, norm_eps, cu_seqlens, lead):
     """Checks the token tensors (`lead` leading dimensions) and fills the options; returns
     (rows' leading shape, H, Hk, N, dtype code, options)."""
-    _need(v.dim() == lead + 2, f"v has {v.dim()} dimensions, expected {lead + 2}")
-    _need(k.dim() == lead + 2, f"k has {k.dim()} dimensions, expected {lead + 2}")
-    dt, dev, shape = _dt(v), v.device, tuple(v.shape[:-2])
-    H, N, Hk = v.shape[-2], v.shape[-1], k.shape[-2]
-    o = DeltaOpts()
-    o.q_stride = _row_stride("q", q, (*shape, Hk, N), v.dtype, dev)
-    o.k_stride = _row_stride("k", k, (*shape, Hk, N), v.dtype, dev)
-    o.v_stride = _row_stride("v", v, (*shape, H, N), v.dtype, dev)
-    _plain("g", g, (*shape, H), v.dtype, dev)
-    _plain("beta", beta, (*shape, H), v.dtype, dev)
+    if v.dim() != lead + 2:
+        raise ValueError(f"v has {v.dim()} dimensions, expected {lead + 2}")
+    if k.dim() != lead + 2:
+        raise ValueError(f"k has {k.dim()} dimensions, expected {lead + 2}")
+    dt, dtype, dev, full = _dt(v), v.dtype, v.device, v.shape
+    shape, H, N = full[:-2], full[-2], full[-1]
+    Hk = k.shape[-2]
+    keys, gates = (*shape, Hk, N), (*shape, H)
+    qs, ks = _row_stride("q", q, keys, dtype, dev), _row_stride("k", k, keys, dtype, dev)
+    vs = _row_stride("v", v, full, dtype, dev)
+    _plain("g", g, gates, dtype, dev)
+    _plain("beta", beta, gates, dtype, dev)
+    cu = None
     if cu_seqlens is not None:
-        _need(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 2, "cu_seqlens needs at least two entries")
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens needs one dimension of at least two entries")
         _plain("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, dev)
-        o.cu_seqlens = cu_seqlens.data_ptr()
-    o.scale = 0.0 if scale is None else float(scale)
-    o.qk_norm, o.norm_eps = int(qk_norm), float(norm_eps)
-    return shape, H, Hk, N, dt, o
+        cu = cu_seqlens.data_ptr()
+    return shape, H, Hk, N, dt, DeltaOpts(0.0 if scale is None else scale, int(qk_norm), norm_eps, cu, qs, ks, vs)
 
 
 def delta_forward(q, k, v, g, beta, S0=None, *, scale=None, qk_norm=False, norm_eps=1e-6, cu_seqlens=None, y=None,
@@ -717,17 +741,19 @@ def delta_forward(q, k, v, g, beta, S0=None, *, scale=None, qk_norm=False, norm_
     dev, states = v.device, (B, H, N, N)
     if S0 is not None:
         _plain("S0", S0, states, torch.float32, dev)
-    with _on(dev, stream) as handle:
+    with _On(dev, stream) as handle:
         if y is None:
             y = (torch.empty if cu_seqlens is None else torch.zeros)(v.shape, device=dev, dtype=v.dtype)
-        _plain("y", y, v.shape, v.dtype, dev)
-        if S_T is None and return_state:
-            S_T = torch.empty(states, device=dev, dtype=torch.float32)
+        else:
+            _plain("y", y, v.shape, v.dtype, dev)
         if S_T is not None:
             _plain("S_T", S_T, states, torch.float32, dev)
-        st = load().wkv7_delta_forward(B, T, H, Hk, N, dt, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0),
-                                       _ptr(y), _ptr(S_T), ctypes.byref(o), handle)
-    _check(st, "wkv7_delta_forward")
+        elif return_state:
+            S_T = torch.empty(states, device=dev, dtype=torch.float32)
+        st = load().wkv7_delta_forward(B, T, H, Hk, N, dt, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                       beta.data_ptr(), _at(S0), y.data_ptr(), _at(S_T), o, handle)
+    if st:
+        _check(st, "wkv7_delta_forward")
     return y, S_T
 
 
@@ -749,25 +775,28 @@ def delta_backward(q, k, v, g, beta, dy, S0=None, dS_T=None, *, scale=None, qk_n
         if t is not None:
             _plain(name, t, states, torch.float32, dev)
     lib = load()
-    with _on(dev, stream) as handle:
-        like = {"dq": q.shape, "dk": k.shape, "dv": v.shape, "dg": g.shape, "dbeta": beta.shape}
+    with _On(dev, stream) as handle:
+        like = (q.shape, k.shape, v.shape, g.shape, beta.shape)
         if grads is None:
             new = torch.empty if cu_seqlens is None else torch.zeros
-            grads = {n: new(s, device=dev, dtype=v.dtype) for n, s in like.items()}
-        for n, s in like.items():
-            _plain(n, grads[n], s, v.dtype, dev)
-        if dS0 is None and return_state_grad:
-            dS0 = torch.empty(states, device=dev, dtype=torch.float32)
+            grads = {n: new(s, device=dev, dtype=v.dtype) for n, s in zip(DELTA_GRAD_NAMES, like)}
+        else:
+            for n, s in zip(DELTA_GRAD_NAMES, like):
+                _plain(n, grads[n], s, v.dtype, dev)
         if dS0 is not None:
             _plain("dS0", dS0, states, torch.float32, dev)
-        need = int(lib.wkv7_delta_backward_workspace_bytes(B, T, H, Hk, N, dt, ctypes.byref(o)))
+        elif return_state_grad:
+            dS0 = torch.empty(states, device=dev, dtype=torch.float32)
+        need = lib.wkv7_delta_backward_workspace_bytes(B, T, H, Hk, N, dt, o)
         if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
             workspace = torch.empty(need, device=dev, dtype=torch.uint8)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = lib.wkv7_delta_backward(B, T, H, Hk, N, dt, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0),
-                                     _ptr(dy), _ptr(dS_T), *(_ptr(grads[n]) for n in DELTA_GRAD_NAMES), _ptr(dS0),
-                                     ctypes.byref(o), _ptr(workspace), ws_bytes, handle)
-    _check(st, "wkv7_delta_backward")
+        st = lib.wkv7_delta_backward(B, T, H, Hk, N, dt, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                     beta.data_ptr(), _at(S0), dy.data_ptr(), _at(dS_T),
+                                     *(grads[n].data_ptr() for n in DELTA_GRAD_NAMES), _at(dS0), o, _at(workspace),
+                                     ws_bytes, handle)
+    if st:
+        _check(st, "wkv7_delta_backward")
     return {**{n: grads[n] for n in DELTA_GRAD_NAMES}, "dS0": dS0}
 
 
@@ -777,17 +806,19 @@ def delta_step(q, k, v, g, beta, S, *, slots=None, scale=None, qk_norm=False, no
     None = row b at slot b). Returns y [B, H, N] of the inputs' type, zero for padding."""
     shape, H, Hk, N, dt, o = _delta_args(q, k, v, g, beta, scale, qk_norm, norm_eps, None, 1)
     B, dev = shape[0], v.device
-    _need(S.dim() == 4, "S needs four dimensions [n_slots, H, N, N]")
-    _plain("S", S, (S.shape[0], H, N, N), torch.float32, dev)
+    n_slots = S.shape[0] if S.dim() == 4 else -1
+    _plain("S", S, (n_slots, H, N, N), torch.float32, dev)
     if slots is not None:
         _plain("slots", slots, (B,), torch.int32, dev)
-    with _on(dev, stream) as handle:
+    with _On(dev, stream) as handle:
         if y is None:
             y = torch.empty(v.shape, device=dev, dtype=v.dtype)
-        _plain("y", y, v.shape, v.dtype, dev)
-        st = load().wkv7_delta_step(B, H, Hk, N, dt, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S),
-                                    S.shape[0], _ptr(slots), _ptr(y), ctypes.byref(o), handle)
-    _check(st, "wkv7_delta_step")
+        else:
+            _plain("y", y, v.shape, v.dtype, dev)
+        st = load().wkv7_delta_step(B, H, Hk, N, dt, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                    beta.data_ptr(), S.data_ptr(), n_slots, _at(slots), y.data_ptr(), o, handle)
+    if st:
+        _check(st, "wkv7_delta_step")
     return y
 
 
@@ -796,30 +827,35 @@ def beam_select(logits, scores, M, *, finished=None, eos=0, out=None, workspace=
     (wkv7_beam_select): logits [B, K, V] bf16 or fp32 (rows may be spaced apart), scores [B, K] fp32,
     finished [B, K] bool or uint8. Returns (scores, parents, tokens), each [B, M] (fp32, int32,
     int32), or fills ``out``, three such tensors."""
-    _need(logits.dim() == 3, "logits needs three dimensions [B, K, V]")
+    if logits.dim() != 3:
+        raise ValueError("logits needs three dimensions [B, K, V]")
     lib, dev, dt = load(), logits.device, _dt(logits)
     B, K, V = logits.shape
     stride = V
     if not logits.is_contiguous():
-        _need(V == 1 or logits.stride(2) == 1, "logits must be dense over the vocabulary")
+        if V != 1 and logits.stride(2) != 1:
+            raise ValueError("logits must be dense over the vocabulary")
         stride = logits.stride(1) if K > 1 else (logits.stride(0) if B > 1 else V)
-        _need(B == 1 or K == 1 or logits.stride(0) == K * stride, "logits: its rows are not evenly spaced")
+        if B > 1 and K > 1 and logits.stride(0) != K * stride:
+            raise ValueError("logits: its rows are not evenly spaced")
     _plain("scores", scores, (B, K), torch.float32, dev)
     if finished is not None:
         _plain("finished", finished, (B, K), torch.bool if finished.dtype == torch.bool else torch.uint8, dev)
-    with _on(dev, stream) as handle:
+    with _On(dev, stream) as handle:
         if out is None:
-            out = (torch.empty((B, M), device=dev, dtype=torch.float32),
-                   torch.empty((B, M), device=dev, dtype=torch.int32), torch.empty((B, M), device=dev, dtype=torch.int32))
-        for n, t, d in zip(("scores", "parents", "tokens"), out, (torch.float32, torch.int32, torch.int32)):
-            _plain("out " + n, t, (B, M), d, dev)
-        need = int(lib.wkv7_beam_select_workspace_bytes(B, K, V, M))
+            out = tuple(torch.empty((B, M), device=dev, dtype=d) for d in (torch.float32, torch.int32, torch.int32))
+        else:
+            for n, t, d in zip(("scores", "parents", "tokens"), out, (torch.float32, torch.int32, torch.int32)):
+                _plain("out " + n, t, (B, M), d, dev)
+        need = lib.wkv7_beam_select_workspace_bytes(B, K, V, M)
         if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
             workspace = torch.empty(need, device=dev, dtype=torch.uint8)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = lib.wkv7_beam_select(B, K, V, M, dt, _ptr(logits), stride, _ptr(scores), _ptr(finished), int(eos),
-                                  *(_ptr(t) for t in out), _ptr(workspace), ws_bytes, handle)
-    _check(st, "wkv7_beam_select")
+        st = lib.wkv7_beam_select(B, K, V, M, dt, logits.data_ptr(), stride, scores.data_ptr(), _at(finished), eos,
+                                  out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), _at(workspace), ws_bytes,
+                                  handle)
+    if st:
+        _check(st, "wkv7_beam_select")
     return tuple(out)
 
 
@@ -827,17 +863,22 @@ def beam_reorder(parents, state, *, batch_dim=0, out=None, stream=None):
     """Moves the rows of ``state`` (contiguous, [.., B, K, ..] with B at batch_dim, any type, the
     bytes of a row a multiple of 16) to the beams that parents [B, K] int32 names, in place or into
     ``out`` (wkv7_beam_reorder). Returns the reordered tensor."""
-    _need(parents.dim() == 2, "parents needs two dimensions [B, K]")
-    dev, (B, K) = state.device, parents.shape
+    if parents.dim() != 2:
+        raise ValueError("parents needs two dimensions [B, K]")
+    dev, shape = state.device, state.shape
+    B, K = parents.shape
     _plain("parents", parents, (B, K), torch.int32, dev)
-    _need(0 <= batch_dim <= state.dim() - 2 and tuple(state.shape[batch_dim:batch_dim + 2]) == (B, K),
-          f"state has shape {tuple(state.shape)}, expected {(B, K)} at dimension {batch_dim}")
-    _need(state.is_contiguous(), "state must be contiguous")
+    if not (0 <= batch_dim <= len(shape) - 2 and shape[batch_dim:batch_dim + 2] == (B, K)):
+        raise ValueError(f"state has shape {tuple(shape)}, expected {(B, K)} at dimension {batch_dim}")
+    if not state.is_contiguous():
+        raise ValueError("state must be contiguous")
     dst = state if out is None else out
-    _plain("out", dst, state.shape, state.dtype, dev)
-    L = math.prod(state.shape[:batch_dim])
-    row = math.prod(state.shape[batch_dim + 2:]) * state.element_size()
-    with _on(dev, stream) as handle:
-        st = load().wkv7_beam_reorder(L, B, K, row, _ptr(parents), _ptr(state), _ptr(dst), handle)
-    _check(st, "wkv7_beam_reorder")
+    if out is not None:
+        _plain("out", out, shape, state.dtype, dev)
+    L = math.prod(shape[:batch_dim])
+    row = math.prod(shape[batch_dim + 2:]) * state.element_size()
+    with _On(dev, stream) as handle:
+        st = load().wkv7_beam_reorder(L, B, K, row, parents.data_ptr(), state.data_ptr(), dst.data_ptr(), handle)
+    if st:
+        _check(st, "wkv7_beam_reorder")
     return dst
