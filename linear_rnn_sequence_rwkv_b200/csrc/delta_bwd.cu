@@ -26,20 +26,20 @@ using namespace dm;
 
 namespace {
 
-template <int NN, int RW, bool F32>
+template <int NN, int RW, bool F32, int GROUPS>
 struct RevLayout {
     static constexpr int TI = F32 ? 3 : 1, TP = 3;
     static constexpr int KB = TI * C * NN * 2, YB = TI * C * RW * 32;
     static constexpr int kK = 0, kQ = KB, kY = 2 * KB, kW = kY + YB, kP = kW + 3 * kTri, kS = kP + TP * kTri;
     static constexpr int stage = (kS + int(sizeof(Scalars)) + 127) / 128 * 128;
-    static constexpr int stages = F32 ? (NN == 64 ? 4 : 3) : (NN == 64 ? 5 : 6);
-    static constexpr int total = stages * stage + kGroups * int(sizeof(PrepScratch));
-    static constexpr int threads = RW * 32 + kGroups * kGroup, meet = RW * 32 + kGroup;
+    static constexpr int stages = F32 ? (NN == 64 ? 4 : 3) : (NN == 64 && GROUPS == 2 ? 5 : 6);
+    static constexpr int total = stages * stage + GROUPS * int(sizeof(PrepScratch));
+    static constexpr int threads = RW * 32 + GROUPS * kGroup, meet = RW * 32 + kGroup;
 };
 
-template <int NN, int RW, bool F32>
-__global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64) ? 2 : 1) delta_reverse_kernel(const DeltaArgs p) {
-    using L = RevLayout<NN, RW, F32>;
+template <int NN, int RW, bool F32, int GROUPS>
+__global__ void __launch_bounds__(RW * 32 + GROUPS * kGroup, (!F32 && NN == 64 && GROUPS == 2) ? 2 : 1) delta_reverse_kernel(const DeltaArgs p) {
+    using L = RevLayout<NN, RW, F32, GROUPS>;
     using Tin = std::conditional_t<F32, float, __nv_bfloat16>;
     constexpr int TI = L::TI, NB = NN * 2, TB = C * NB, YNB = RW * 32, YTB = C * YNB;
     extern __shared__ __align__(128) unsigned char sm[];
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
     delta_rows(p.cu, p.T, s, t0, t1);
     const int chunks = int((t1 - t0 + C - 1) / C);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int full = 1 + kGroups, empty = full + L::stages;
+    constexpr int full = GROUPS, empty = full + L::stages;       // named barriers; 0 .. GROUPS - 1: the groups' own
 
     // step r takes chunk chunks - 1 - r
     if (warp >= RW) {
@@ -70,27 +70,27 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
             k.load(st + L::kK, n);
             q.load(st + L::kQ, n);
             dy.load(st + L::kY, n);
-            k.advance(-kGroups);
-            q.advance(-kGroups);
-            dy.advance(-kGroups);
+            k.advance(-GROUPS);
+            q.advance(-GROUPS);
+            dy.advance(-GROUPS);
             cp_commit();
         };
         if (group < chunks) load(group);
-        for (int r = group; r < chunks; r += kGroups) {
+        for (int r = group; r < chunks; r += GROUPS) {
             gate = next;
-            if (r + kGroups < chunks) {
-                if (r + kGroups >= L::stages) bar_sync(empty + (r + kGroups) % L::stages, L::meet);
-                load(r + kGroups);
+            if (r + GROUPS < chunks) {
+                if (r + GROUPS >= L::stages) bar_sync(empty + (r + GROUPS) % L::stages, L::meet);
+                load(r + GROUPS);
                 cp_wait<1>();
             } else {
                 cp_wait<0>();
             }
-            bar_sync(1 + group, kGroup);
+            bar_sync(group, kGroup);
             unsigned char *st = sm + (r % L::stages) * L::stage;
             const uint32_t sa = base + (r % L::stages) * L::stage;
-            const bool queries = ((warp ^ (r / kGroups)) & 1) != 0;
+            const bool queries = ((warp ^ (r / GROUPS)) & 1) != 0;
             prepare_chunk<NN, TI, 3>(sa + L::kK, sa + L::kQ, st + L::kW, sa + L::kP, reinterpret_cast<Scalars *>(st + L::kS), ps, p,
-                                     delta_clamp(gate.num(gate.g)), gate.num(gate.beta), queries, 1 + group);
+                                     delta_clamp(gate.num(gate.g)), gate.num(gate.beta), queries, group);
             bar_arrive(full + r % L::stages, L::meet);
         }
         return;
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
 #pragma unroll
             for (int n = 0; n < NN / 16; ++n) {
                 uint32_t b[2][TI][4];
-                float d[2][4] = {};
+                float d[2][4];
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -229,6 +229,11 @@ __global__ void __launch_bounds__(RW * 32 + kGroups * kGroup, (!F32 && NN == 64)
                         if (x + z > 2) continue;
 #pragma unroll
                         for (int kb = 0; kb < 2; ++kb) {
+                            if (x == 2 && z == 0 && kb == 0) {
+                                mma0(d[0], u[kb][x], b[kb][z][0], b[kb][z][1]);
+                                mma0(d[1], u[kb][x], b[kb][z][2], b[kb][z][3]);
+                                continue;
+                            }
                             mma(d[0], u[kb][x], b[kb][z][0], b[kb][z][1]);
                             mma(d[1], u[kb][x], b[kb][z][2], b[kb][z][3]);
                         }
@@ -785,11 +790,11 @@ cudaError_t allow_dynamic_smem(const void *kernel, int bytes);
 
 namespace {
 
-template <int NN, int RW, bool F32>
+template <int NN, int RW, bool F32, int GROUPS>
 cudaError_t launch_t(const DeltaArgs &p, long long slots) {
-    using R = RevLayout<NN, RW, F32>;
+    using R = RevLayout<NN, RW, F32, GROUPS>;
     constexpr int grad_bytes = GradLayout<NN, F32>::kF + int(sizeof(GradScalars));
-    const void *rev = reinterpret_cast<const void *>(delta_reverse_kernel<NN, RW, F32>);
+    const void *rev = reinterpret_cast<const void *>(delta_reverse_kernel<NN, RW, F32, GROUPS>);
     const void *grad = reinterpret_cast<const void *>(delta_grad_kernel<NN, F32>);
     cudaError_t e = allow_dynamic_smem(rev, R::total);
     if (e != cudaSuccess) return e;
@@ -797,7 +802,7 @@ cudaError_t launch_t(const DeltaArgs &p, long long slots) {
     if (e != cudaSuccess) return e;
     e = launch_delta_states(p);
     if (e != cudaSuccess) return e;
-    delta_reverse_kernel<NN, RW, F32><<<unsigned(p.B) * p.H * (NN / (16 * RW)), R::threads, R::total, p.stream>>>(p);
+    delta_reverse_kernel<NN, RW, F32, GROUPS><<<unsigned(p.B) * p.H * (NN / (16 * RW)), R::threads, R::total, p.stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     delta_grad_kernel<NN, F32><<<unsigned(slots) * p.Hk, GT, grad_bytes, p.stream>>>(p);
@@ -825,8 +830,9 @@ cudaError_t launch_delta_backward(const DeltaArgs &p0) {
     p.keep_S = ws;
     p.keep_dS = ws + (p.dt == WKV7_BF16 ? 2 : 1) * state;
     p.keep_second = (long long)(state / el);
-    if (p.dt == WKV7_F32) return p.N == 64 ? launch_t<64, 4, true>(p, slots) : launch_t<128, 4, true>(p, slots);
-    return p.N == 64 ? launch_t<64, 4, false>(p, slots) : launch_t<128, 8, false>(p, slots);
+    if (p.dt == WKV7_F32) return p.N == 64 ? launch_t<64, 4, true, 2>(p, slots) : launch_t<128, 4, true, 2>(p, slots);
+    if (p.N == 128) return launch_t<128, 4, false, 2>(p, slots);
+    return (long long)p.B * p.H <= 74 ? launch_t<64, 2, false, 3>(p, slots) : launch_t<64, 4, false, 2>(p, slots);
 }
 
 }  // namespace wkv7

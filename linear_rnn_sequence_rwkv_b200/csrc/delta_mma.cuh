@@ -22,7 +22,6 @@ namespace dm {
 
 constexpr int C = 32;               // tokens per chunk
 constexpr int kGroup = 64;          // threads that prepare one chunk: a warp for the keys, one for the queries
-constexpr int kGroups = 2;          // chunks prepared at a time
 constexpr int kTri = 3 * 512;       // bytes of one term of a lower triangular [32][32]: blocks (0,0), (1,0), (1,1)
 constexpr int kAs = 20;             // row of a 16 x 16 fp32 scratch block, two of which lie where W goes
 constexpr int kAb = 16 * kAs + 16;  // from one block to the next, in other banks
@@ -48,6 +47,12 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// d = a b
+__device__ __forceinline__ void mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
@@ -60,6 +65,9 @@ __device__ __forceinline__ void st_v4(uint32_t a, uint32_t x, uint32_t y, uint32
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
+__device__ __forceinline__ void ld_v4(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
 __device__ __forceinline__ void st_b32(uint32_t a, uint32_t x) { asm volatile("st.shared.b32 [%0], %1;" :: "r"(a), "r"(x) : "memory"); }
 
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
@@ -277,50 +285,58 @@ __device__ __forceinline__ void prepare_chunk(uint32_t k, uint32_t q, unsigned c
     float len[4] = {};
     if (TP > 0 || !queries) {
 #pragma unroll 1
-    for (int ks = 0; ks < NN / 16; ++ks) {
-        uint32_t a0[TI][4], a1[TI][4], b0[TI][4], b1[TI][4];
+        for (int ks = 0; ks < NN / 16; ++ks) {
+            uint32_t a0[TI][4], a1[TI][4], b0[TI][4], b1[TI][4];
 #pragma unroll
-        for (int i = 0; i < TI; ++i) {
-            ldsm4(a0[i], addr_a<NB>(left + i * TB, 0, ks));
-            ldsm4(a1[i], addr_a<NB>(left + i * TB, 16, ks));
-            ldsm4(b0[i], addr_b<NB>(k + i * TB, 0, ks));
-            ldsm4(b1[i], addr_b<NB>(k + i * TB, 16, ks));
-        }
-#pragma unroll
-        for (int x = TI - 1; x >= 0; --x)
-#pragma unroll
-            for (int y = TI - 1 - x; y >= 0; --y) {
-                const bool top = x + y == 0;
-                prod.add(0, top, a0[x], b0[y][0], b0[y][1]);
-                prod.add(1, top, a0[x], b0[y][2], b0[y][3]);
-                prod.add(2, top, a1[x], b0[y][0], b0[y][1]);
-                prod.add(3, top, a1[x], b0[y][2], b0[y][3]);
-                prod.add(4, top, a1[x], b1[y][0], b1[y][1]);
-                prod.add(5, top, a1[x], b1[y][2], b1[y][3]);
+            for (int i = 0; i < TI; ++i) {
+                ldsm4(a0[i], addr_a<NB>(left + i * TB, 0, ks));
+                ldsm4(a1[i], addr_a<NB>(left + i * TB, 16, ks));
+                ldsm4(b0[i], addr_b<NB>(k + i * TB, 0, ks));
+                ldsm4(b1[i], addr_b<NB>(k + i * TB, 16, ks));
             }
-        // the rows' squares from the same fragments: rows gr, gr + 8, 16 + gr, 24 + gr
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+            for (int x = TI - 1; x >= 0; --x)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float x = 0.f, y = 0.f;
-#pragma unroll
-                for (int i = TI - 1; i >= 0; --i) {
-                    const uint32_t u = (r < 2 ? a0[i] : a1[i])[(r & 1) + 2 * c];
-                    x += lo_f(u);
-                    y += hi_f(u);
+                for (int y = TI - 1 - x; y >= 0; --y) {
+                    const bool top = x + y == 0;
+                    prod.add(0, top, a0[x], b0[y][0], b0[y][1]);
+                    prod.add(1, top, a0[x], b0[y][2], b0[y][3]);
+                    prod.add(2, top, a1[x], b0[y][0], b0[y][1]);
+                    prod.add(3, top, a1[x], b0[y][2], b0[y][3]);
+                    prod.add(4, top, a1[x], b1[y][0], b1[y][1]);
+                    prod.add(5, top, a1[x], b1[y][2], b1[y][3]);
                 }
-                len[r] = fmaf(x, x, fmaf(y, y, len[r]));
-            }
-    }
+            if (!queries) continue;     // the keys' squares are the products' diagonal
+            // the queries' from the same fragments: rows gr, gr + 8, 16 + gr, 24 + gr
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        len[r] += __shfl_xor_sync(0xffffffffu, len[r], 1);
-        len[r] += __shfl_xor_sync(0xffffffffu, len[r], 2);
-    }
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float x = 0.f, y = 0.f;
+#pragma unroll
+                    for (int i = TI - 1; i >= 0; --i) {
+                        const uint32_t u = (r < 2 ? a0[i] : a1[i])[(r & 1) + 2 * c];
+                        x += lo_f(u);
+                        y += hi_f(u);
+                    }
+                    len[r] = fmaf(x, x, fmaf(y, y, len[r]));
+                }
+        }
     }
     prod.join();
-    if (!queries) {
+    if (queries) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            len[r] += __shfl_xor_sync(0xffffffffu, len[r], 1);
+            len[r] += __shfl_xor_sync(0xffffffffu, len[r], 2);
+        }
+    } else {                        // row gr of a diagonal tile is its column 2 tc + e where tc = gr / 2, e = gr % 2
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float (&d)[4] = acc[r < 2 ? r : r + 2];
+            const float x = d[2 * (r & 1)], y = d[2 * (r & 1) + 1];
+            len[r] = __shfl_sync(0xffffffffu, gr & 1 ? y : x, 4 * gr + (gr >> 1));
+        }
         const bool fine = len[0] + len[1] + len[2] + len[3] < INFINITY && g <= 80.f && fabsf(beta) < INFINITY;
         const bool odd = __any_sync(0xffffffffu, !fine);
         if (lane == 0) sc->odd = odd;
@@ -357,7 +373,33 @@ __device__ __forceinline__ void prepare_chunk(uint32_t k, uint32_t q, unsigned c
         if (lane == 31) sc->whole = nan ? bad : in;
         if constexpr (TP == 0) return;
     }
-    {   // D and the factors of rows and columns: rows gr + 8 i, columns 8 n + 2 tc, + 1
+    // D and the factors of rows and columns. Where the chunk's sums stay within 30 of the middle one, D is a
+    // product of a row's and a column's factor, two exponentials per token; elsewhere one per element.
+    const int last = queries ? 0 : -1;          // column j of row i stays if j <= i + last
+    const long long off = G - __shfl_sync(0xffffffffu, G, C / 2 - 1);
+    const bool near = __all_sync(0xffffffffu, off < (30ll << 32) && off > -(30ll << 32));
+    if (near) {
+        const float hi = float(int(off >> 22)) * 9.765625e-4f, lo = float(int(off & 0x3fffff)) * 2.3283064365386963e-10f;
+        const float up = expf(hi), down = expf(-hi);
+        const float l2 = 0.5f * lo * lo;        // exp(lo) = 1 + lo + lo^2 / 2: lo is below 2^-10
+        const float row = (seen ? bad : fmaf(up, lo + l2, up)) * (queries ? ps->rq : ps->rk)[lane];
+        const float col = (seen ? bad : fmaf(down, l2 - lo, down)) * kb;
+        float rf[4], cf[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rf[i] = __shfl_sync(0xffffffffu, row, gr + 8 * i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) cf[j] = __shfl_sync(0xffffffffu, col, 8 * (j >> 1) + 2 * tc + (j & 1));
+#pragma unroll
+        for (int x = 0; x < 6; ++x) {
+            const int m = x < 2 ? 0 : 1, n = x < 2 ? x : x - 2;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int ri = 2 * m + (e >> 1), ci = 2 * n + (e & 1);
+                const float w = acc[x][e] * cf[ci] * rf[ri];
+                acc[x][e] = 8 * n + 2 * tc + (e & 1) <= gr + 8 * ri + last ? w : 0.f;
+            }
+        }
+    } else {
         float rh[4], rl[4], ch[8], cl[8], cb[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -371,7 +413,6 @@ __device__ __forceinline__ void prepare_chunk(uint32_t k, uint32_t q, unsigned c
             cl[j] = __shfl_sync(0xffffffffu, glo, from);
             cb[j] = __shfl_sync(0xffffffffu, kb, from);
         }
-        const int last = queries ? 0 : -1;      // column j of row i stays if j <= i + last
 #pragma unroll
         for (int x = 0; x < 6; ++x) {
             const int m = x < 2 ? 0 : 1, n = x < 2 ? x : x - 2;
