@@ -1,11 +1,12 @@
-// The gated delta rule's backward, in three kernels. With the chunk quantities of delta_chunk.cu and
+// The gated delta rule's backward, in two kernels. With the chunk quantities of delta_sweep.cuh and
 // dS' the gradient of a chunk's last state:
-//   1. delta_chunk_kernel with STATES (delta_chunk.cu): the errors E, and the state every 64 tokens start from.
-//   2. delta_reverse_kernel: the chain back through the chunks of 32,
+//   1. the forward sweep (delta_sweep.cuh, STATES): the errors E, and the state every 64 tokens start from;
+//   2. the reverse sweep: the chain back through the chunks of 32,
 //          dE = P^T dY + out (K dS'^T),   dX = W^T dE,   dV = dX,
 //          dS = exp(G_C) dS' + (qin dY)^T Q - (kin dX)^T K
 //      (out, qin, kin: the scalars of delta_mma.cuh). As forward, the rows of dS never meet: a warp owns 16 of
-//      them, in accumulators, and the chain runs through its registers.
+//      them, in accumulators, and the chain runs through its registers. Neither sweep needs anything of the other, so
+//      that one launch may run both (delta_sweeps_kernel);
 //   3. delta_grad_kernel: everything that contracts over the value channels, for all chunks of 64 at once:
 //          A = dY E^T (j <= i), B = dX E^T (j < i), n = sq_i rk_j D beta_j A, o = rk_i rk_j D beta_j B
 //          sq dQ = n K + qin (dY S),    rk dK = n^T Q - o K - o^T K + out (E dS') - kin (dX S)
@@ -18,7 +19,7 @@
 // Precision: the chain of dS keeps three bf16 terms wherever a state or its gradient is read or written. For
 // outputs in bf16, everything computed (E, dX, S, dS', n, o) enters the sums in two terms, 16 bits: dg is a
 // difference of large sums and would show a single term's rounding several times over.
-#include "delta_mma.cuh"
+#include "delta_sweep.cuh"
 
 namespace wkv7 {
 
@@ -38,15 +39,15 @@ struct RevLayout {
 };
 
 template <int NN, int RW, bool F32, int GROUPS>
-__global__ void __launch_bounds__(RW * 32 + GROUPS * kGroup, (!F32 && NN == 64 && GROUPS == 2) ? 2 : 1) delta_reverse_kernel(const DeltaArgs p) {
+__device__ __forceinline__ void reverse_sweep(const DeltaArgs &p, unsigned block) {
     using L = RevLayout<NN, RW, F32, GROUPS>;
     using Tin = std::conditional_t<F32, float, __nv_bfloat16>;
     constexpr int TI = L::TI, NB = NN * 2, TB = C * NB, YNB = RW * 32, YTB = C * YNB;
     extern __shared__ __align__(128) unsigned char sm[];
     const uint32_t base = smem_addr(sm);
     constexpr int slices = NN / (16 * RW);
-    const unsigned unit = blockIdx.x / slices;
-    const int row0 = (blockIdx.x % slices) * 16 * RW;
+    const unsigned unit = block / slices;
+    const int row0 = (block % slices) * 16 * RW;
     const int s = unit / unsigned(p.H), h = unit % unsigned(p.H), hk = h / (p.H / p.Hk);
     long long t0, t1;
     delta_rows(p.cu, p.T, s, t0, t1);
@@ -292,6 +293,14 @@ __global__ void __launch_bounds__(RW * 32 + GROUPS * kGroup, (!F32 && NN == 64 &
             *reinterpret_cast<float2 *>(p.dS0 + so + (gr + 8) * NN + 8 * n + 2 * tc) = make_float2(S[n][2], S[n][3]);
         }
     }
+}
+
+template <int NN, int RW, bool F32, int GROUPS>
+__global__ void __launch_bounds__(RW * 32 + GROUPS * kGroup, (!F32 && NN == 64 && GROUPS == 2) ? 2 : 1) delta_sweeps_kernel(const DeltaArgs p, int which) {
+    const bool both = which == 2;                       // else 0: the reverse sweep, 1: the forward one
+    const unsigned block = both ? blockIdx.x >> 1 : blockIdx.x;
+    if (both ? blockIdx.x & 1 : which) forward_sweep<NN, RW, F32, true, GROUPS>(p, block);
+    else reverse_sweep<NN, RW, F32, GROUPS>(p, block);
 }
 
 // ---- the gradients of a chunk of 64 tokens ------------------------------------------------------------
@@ -792,19 +801,25 @@ namespace {
 
 template <int NN, int RW, bool F32, int GROUPS>
 cudaError_t launch_t(const DeltaArgs &p, long long slots) {
-    using R = RevLayout<NN, RW, F32, GROUPS>;
+    constexpr int fwd_bytes = Layout<NN, RW, F32, true, GROUPS>::total, rev_bytes = RevLayout<NN, RW, F32, GROUPS>::total;
+    constexpr int sweep_bytes = fwd_bytes > rev_bytes ? fwd_bytes : rev_bytes;
     constexpr int grad_bytes = GradLayout<NN, F32>::kF + int(sizeof(GradScalars));
-    const void *rev = reinterpret_cast<const void *>(delta_reverse_kernel<NN, RW, F32, GROUPS>);
+    const void *sweeps = reinterpret_cast<const void *>(delta_sweeps_kernel<NN, RW, F32, GROUPS>);
     const void *grad = reinterpret_cast<const void *>(delta_grad_kernel<NN, F32>);
-    cudaError_t e = allow_dynamic_smem(rev, R::total);
+    cudaError_t e = allow_dynamic_smem(sweeps, sweep_bytes);
     if (e != cudaSuccess) return e;
     e = allow_dynamic_smem(grad, grad_bytes);
     if (e != cudaSuccess) return e;
-    e = launch_delta_states(p);
-    if (e != cudaSuccess) return e;
-    delta_reverse_kernel<NN, RW, F32, GROUPS><<<unsigned(p.B) * p.H * (NN / (16 * RW)), R::threads, R::total, p.stream>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    // Together where that fills SMs that one sweep leaves idle (and at N = 128, where a CTA has an SM to itself:
+    // 541 us against 584 for seven packed sequences of 8 heads); in turn otherwise, since blocks of the two kinds
+    // on one SM crowd each other's instructions out (96 heads of N = 64: 320 us against 267).
+    const unsigned blocks = unsigned(p.B) * p.H * (NN / (16 * RW));
+    const bool both = NN == 128 || blocks <= 74;
+    for (int which = both ? 2 : 1; which >= (both ? 2 : 0); --which) {
+        delta_sweeps_kernel<NN, RW, F32, GROUPS><<<both ? 2 * blocks : blocks, RW * 32 + GROUPS * kGroup, sweep_bytes, p.stream>>>(p, which);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
     delta_grad_kernel<NN, F32><<<unsigned(slots) * p.Hk, GT, grad_bytes, p.stream>>>(p);
     return cudaGetLastError();
 }
@@ -832,7 +847,7 @@ cudaError_t launch_delta_backward(const DeltaArgs &p0) {
     p.keep_second = (long long)(state / el);
     if (p.dt == WKV7_F32) return p.N == 64 ? launch_t<64, 4, true, 2>(p, slots) : launch_t<128, 4, true, 2>(p, slots);
     if (p.N == 128) return launch_t<128, 4, false, 2>(p, slots);
-    return (long long)p.B * p.H <= 74 ? launch_t<64, 2, false, 3>(p, slots) : launch_t<64, 4, false, 2>(p, slots);
+    return (long long)p.B * p.H <= 37 ? launch_t<64, 2, false, 3>(p, slots) : launch_t<64, 4, false, 2>(p, slots);     // as forward, twice the blocks
 }
 
 }  // namespace wkv7
