@@ -154,19 +154,20 @@ __device__ __forceinline__ void reverse_sweep(const DeltaArgs &p, unsigned block
         for (int ib = 0; ib < 2; ++ib) {
 #pragma unroll
             for (int i = 0; i < TI; ++i) ldsm4t(y[ib][i], st + L::kY + i * YTB + tile<YNB>(16 * ib + tok_l, col_l));
+            uint32_t w[2][3][4];
 #pragma unroll
-            for (int jb = 0; jb <= ib; ++jb) {
-                uint32_t w[3][4];
+            for (int jb = 0; jb <= ib; ++jb)
 #pragma unroll
-                for (int z = 0; z < 3; ++z) ldsm4t(w[z], addr_block_t(st + L::kP + z * kTri + (ib + jb) * 512));
+                for (int z = 0; z < 3; ++z) ldsm4t(w[jb][z], addr_block_t(st + L::kP + z * kTri + (ib + jb) * 512));
 #pragma unroll
-                for (int x = TI - 1; x >= 0; --x)
+            for (int x = TI - 1; x >= 0; --x)
 #pragma unroll
-                    for (int z = 2 - x; z >= 0; --z) {
-                        ea.add(2 * jb, x + z == 0, y[ib][x], w[z][0], w[z][1]);
-                        ea.add(2 * jb + 1, x + z == 0, y[ib][x], w[z][2], w[z][3]);
+                for (int z = 2 - x; z >= 0; --z)
+#pragma unroll
+                    for (int jb = 0; jb <= ib; ++jb) {
+                        ea.add(2 * jb, x + z == 0, y[ib][x], w[jb][z][0], w[jb][z][1]);
+                        ea.add(2 * jb + 1, x + z == 0, y[ib][x], w[jb][z][2], w[jb][z][3]);
                     }
-            }
         }
         ea.join();
         // dX^T = dE^T W
@@ -174,19 +175,20 @@ __device__ __forceinline__ void reverse_sweep(const DeltaArgs &p, unsigned block
         for (int kb = 0; kb < 2; ++kb) {
             uint32_t a[3][4];
             split_a<3>(E[2 * kb], E[2 * kb + 1], a);
+            uint32_t w[2][3][4];
 #pragma unroll
-            for (int jb = 0; jb <= kb; ++jb) {
-                uint32_t w[3][4];
+            for (int jb = 0; jb <= kb; ++jb)
 #pragma unroll
-                for (int z = 0; z < 3; ++z) ldsm4t(w[z], addr_block_t(st + L::kW + z * kTri + (kb + jb) * 512));
+                for (int z = 0; z < 3; ++z) ldsm4t(w[jb][z], addr_block_t(st + L::kW + z * kTri + (kb + jb) * 512));
 #pragma unroll
-                for (int x = 2; x >= 0; --x)
+            for (int x = 2; x >= 0; --x)
 #pragma unroll
-                    for (int z = 2 - x; z >= 0; --z) {
-                        xa.add(2 * jb, x + z == 0, a[x], w[z][0], w[z][1]);
-                        xa.add(2 * jb + 1, x + z == 0, a[x], w[z][2], w[z][3]);
+                for (int z = 2 - x; z >= 0; --z)
+#pragma unroll
+                    for (int jb = 0; jb <= kb; ++jb) {
+                        xa.add(2 * jb, x + z == 0, a[x], w[jb][z][0], w[jb][z][1]);
+                        xa.add(2 * jb + 1, x + z == 0, a[x], w[jb][z][2], w[jb][z][3]);
                     }
-            }
         }
         xa.join();
         // dS <- exp(G_C) dS + (qin dY)^T Q - (kin dX)^T K: each sum on its own, small products first
@@ -215,35 +217,44 @@ __device__ __forceinline__ void reverse_sweep(const DeltaArgs &p, unsigned block
                 split_a<3>(w[0], w[1], u[kb]);
             }
             const uint32_t right = st + (part ? L::kK : L::kQ);
+            constexpr int NP = TI == 1 ? 2 : 1;     // 16 or 32 key channels at a time: four accumulators
 #pragma unroll
-            for (int n = 0; n < NN / 16; ++n) {
-                uint32_t b[2][TI][4];
-                float d[2][4];
+            for (int n = 0; n < NN / 16; n += NP) {
+                uint32_t b[NP][2][TI][4];
+                float d[NP][2][4];
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
+                for (int m = 0; m < NP; ++m)
 #pragma unroll
-                    for (int z = 0; z < TI; ++z) ldsm4t(b[kb][z], addr_bt<NB>(right + z * TB, 16 * kb, 2 * n));
+                    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                        for (int z = 0; z < TI; ++z) ldsm4t(b[m][kb][z], addr_bt<NB>(right + z * TB, 16 * kb, 2 * (n + m)));
 #pragma unroll
                 for (int x = 2; x >= 0; --x)
 #pragma unroll
                     for (int z = TI - 1; z >= 0; --z) {
                         if (x + z > 2) continue;
 #pragma unroll
-                        for (int kb = 0; kb < 2; ++kb) {
-                            if (x == 2 && z == 0 && kb == 0) {
-                                mma0(d[0], u[kb][x], b[kb][z][0], b[kb][z][1]);
-                                mma0(d[1], u[kb][x], b[kb][z][2], b[kb][z][3]);
-                                continue;
+                        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                            for (int m = 0; m < NP; ++m) {
+                                if (x == 2 && z == 0 && kb == 0) {
+                                    mma0(d[m][0], u[kb][x], b[m][kb][z][0], b[m][kb][z][1]);
+                                    mma0(d[m][1], u[kb][x], b[m][kb][z][2], b[m][kb][z][3]);
+                                } else {
+                                    mma(d[m][0], u[kb][x], b[m][kb][z][0], b[m][kb][z][1]);
+                                    mma(d[m][1], u[kb][x], b[m][kb][z][2], b[m][kb][z][3]);
+                                }
                             }
-                            mma(d[0], u[kb][x], b[kb][z][0], b[kb][z][1]);
-                            mma(d[1], u[kb][x], b[kb][z][2], b[kb][z][3]);
-                        }
                     }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    S[2 * n][e] = part ? S[2 * n][e] + d[0][e] : fmaf(whole, S[2 * n][e], d[0][e]);
-                    S[2 * n + 1][e] = part ? S[2 * n + 1][e] + d[1][e] : fmaf(whole, S[2 * n + 1][e], d[1][e]);
-                }
+                for (int m = 0; m < NP; ++m)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float &x = S[2 * (n + m) + i][e];
+                            x = part ? x + d[m][i][e] : fmaf(whole, x, d[m][i][e]);
+                        }
             }
         }
         if constexpr (F32) {
