@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kPickT) beam_pick_kernel(const BeamArgs p, int
         if (top > -INFINITY)
             for (int s = lane; s < splits; s += 32)
                 if (part[j * splits + s].top > -INFINITY)
-                    sum += part[j * splits + s].sum * exp(double(part[j * splits + s].top) - double(top));
+                    sum += part[j * splits + s].sum * double(expf(part[j * splits + s].top - top));
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) s_norm[j] = double(top) + log(sum);      // NaN where the row has +inf or nothing
@@ -380,9 +380,15 @@ __global__ void __launch_bounds__(kPickT) beam_pick_kernel(const BeamArgs p, int
         const unsigned long long *row = lists + size_t(j) * per_row;
         const unsigned long long key = row[r];
         if (!key) continue;
-        int rank = r - s * M;
-        for (int o = 0; o < splits && rank < M; ++o)
-            if (o != s && row[o * M] > key) rank += count_above(row + o * M, M, key);
+        int rank = r - s * M, heads = 0;                   // lists whose first element precedes this one
+#pragma unroll 8
+        for (int o = 0; o < splits; ++o) heads += o != s && row[o * M] > key;
+        if (rank + heads >= M) continue;
+        for (int o = 0; heads; ++o)
+            if (o != s && row[o * M] > key) {
+                rank += count_above(row + o * M, M, key);
+                --heads;
+            }
         if (rank < M) best[j * M + rank] = key;
     }
     __syncthreads();

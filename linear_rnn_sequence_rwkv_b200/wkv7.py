@@ -707,25 +707,35 @@ def _row_stride(name, t, shape, dtype, dev):
 def _delta_args(q, k, v, g, beta, scale, qk_norm, norm_eps, cu_seqlens, lead):
     """Checks the token tensors (`lead` leading dimensions) and fills the options; returns
     (rows' leading shape, H, Hk, N, dtype code, options)."""
-    if v.dim() != lead + 2:
-        raise ValueError(f"v has {v.dim()} dimensions, expected {lead + 2}")
-    if k.dim() != lead + 2:
-        raise ValueError(f"k has {k.dim()} dimensions, expected {lead + 2}")
-    dt, dtype, dev, full = _dt(v), v.dtype, v.device, v.shape
-    shape, H, N = full[:-2], full[-2], full[-1]
-    Hk = k.shape[-2]
-    keys, gates = (*shape, Hk, N), (*shape, H)
-    qs, ks = _row_stride("q", q, keys, dtype, dev), _row_stride("k", k, keys, dtype, dev)
-    vs = _row_stride("v", v, full, dtype, dev)
-    _plain("g", g, gates, dtype, dev)
-    _plain("beta", beta, gates, dtype, dev)
+    full, ks, dtype = v.shape, k.shape, v.dtype
+    if len(full) != lead + 2:
+        raise ValueError(f"v has {len(full)} dimensions, expected {lead + 2}")
+    if len(ks) != lead + 2:
+        raise ValueError(f"k has {len(ks)} dimensions, expected {lead + 2}")
+    dt, shape, H, N, Hk, on = _dt(v), full[:-2], full[-2], full[-1], ks[-2], v.get_device()
+    qs = ks_ = vs = 0
+    if not (q.shape == ks and ks == (*shape, Hk, N) and g.shape == full[:-1] and beta.shape == full[:-1]
+            and q.dtype is dtype and k.dtype is dtype and g.dtype is dtype and beta.dtype is dtype
+            and q.get_device() == on and k.get_device() == on and g.get_device() == on and beta.get_device() == on
+            and q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and g.is_contiguous()
+            and beta.is_contiguous()):          # strided rows, or something to refuse by name
+        dev, keys = v.device, (*shape, Hk, N)
+        qs, ks_ = _row_stride("q", q, keys, dtype, dev), _row_stride("k", k, keys, dtype, dev)
+        vs = _row_stride("v", v, full, dtype, dev)
+        _plain("g", g, (*shape, H), dtype, dev)
+        _plain("beta", beta, (*shape, H), dtype, dev)
     cu = None
     if cu_seqlens is not None:
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens needs one dimension of at least two entries")
-        _plain("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, dev)
+        _plain("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, v.device)
         cu = cu_seqlens.data_ptr()
-    return shape, H, Hk, N, dt, DeltaOpts(0.0 if scale is None else scale, int(qk_norm), norm_eps, cu, qs, ks, vs)
+    return shape, H, Hk, N, dt, DeltaOpts(0.0 if scale is None else scale, int(qk_norm), norm_eps, cu, qs, ks_, vs)
+
+
+def _like(t):
+    """A new dense tensor of t's shape, type and device (the short way where t is dense itself)."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def delta_forward(q, k, v, g, beta, S0=None, *, scale=None, qk_norm=False, norm_eps=1e-6, cu_seqlens=None, y=None,
@@ -743,13 +753,13 @@ def delta_forward(q, k, v, g, beta, S0=None, *, scale=None, qk_norm=False, norm_
         _plain("S0", S0, states, torch.float32, dev)
     with _On(dev, stream) as handle:
         if y is None:
-            y = (torch.empty if cu_seqlens is None else torch.zeros)(v.shape, device=dev, dtype=v.dtype)
+            y = _like(v) if cu_seqlens is None else torch.zeros(v.shape, device=dev, dtype=v.dtype)
         else:
             _plain("y", y, v.shape, v.dtype, dev)
         if S_T is not None:
             _plain("S_T", S_T, states, torch.float32, dev)
         elif return_state:
-            S_T = torch.empty(states, device=dev, dtype=torch.float32)
+            S_T = torch.empty(states, device=dev, dtype=torch.float32) if S0 is None else torch.empty_like(S0)
         st = load().wkv7_delta_forward(B, T, H, Hk, N, dt, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
                                        beta.data_ptr(), _at(S0), y.data_ptr(), _at(S_T), o, handle)
     if st:
@@ -812,7 +822,7 @@ def delta_step(q, k, v, g, beta, S, *, slots=None, scale=None, qk_norm=False, no
         _plain("slots", slots, (B,), torch.int32, dev)
     with _On(dev, stream) as handle:
         if y is None:
-            y = torch.empty(v.shape, device=dev, dtype=v.dtype)
+            y = _like(v)
         else:
             _plain("y", y, v.shape, v.dtype, dev)
         st = load().wkv7_delta_step(B, H, Hk, N, dt, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
@@ -843,7 +853,8 @@ def beam_select(logits, scores, M, *, finished=None, eos=0, out=None, workspace=
         _plain("finished", finished, (B, K), torch.bool if finished.dtype == torch.bool else torch.uint8, dev)
     with _On(dev, stream) as handle:
         if out is None:
-            out = tuple(torch.empty((B, M), device=dev, dtype=d) for d in (torch.float32, torch.int32, torch.int32))
+            parents = torch.empty((B, M), device=dev, dtype=torch.int32)
+            out = (scores.new_empty((B, M)), parents, torch.empty_like(parents))
         else:
             for n, t, d in zip(("scores", "parents", "tokens"), out, (torch.float32, torch.int32, torch.int32)):
                 _plain("out " + n, t, (B, M), d, dev)

@@ -76,6 +76,27 @@ def test_select_masked_and_bad_rows(cuda_device, dt):
     assert np.all(np.isneginf(got[0])) and np.all(got[1] == -1) and np.all(got[2] == -1)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [(1, 2), (40, 16)])       # one block per CTA, and a whole row
+@pytest.mark.parametrize("M", [1, 16, 33, 64])
+def test_select_orders_that_fill_the_buffer(cuda_device, rows, M, dt):
+    """Rising logits (every block holds only better ones), rising in steps of equal values, falling, all
+    equal, and a few tokens among masked ones: what is gathered overflows, or the floor never rises."""
+    B, K = rows
+    V = 40_003
+    up = torch.arange(V, dtype=torch.float32) / 400
+    kinds = [up, torch.floor(up), -up, torch.zeros(V), torch.where(torch.arange(V) % 3001 == 0, up, float("-inf")),
+             torch.where(torch.arange(V) < 9000, float("-inf"), torch.floor(up)),
+             torch.where(torch.arange(V) > 20000, torch.tensor(torch.finfo(DT[dt]).min), torch.zeros(()))]
+    x = torch.stack([kinds[i % len(kinds)] for i in range(B * K)]).reshape(B, K, V).to(DT[dt])
+    s = torch.arange(B * K, dtype=torch.float32).reshape(B, K) / 8
+    got = pick(cuda_device, x, s, M)
+    some = range(B) if B < 8 else (0, 1, 2, 3, B - 1)
+    ref = delta.beam_select(x[list(some)].double().numpy(), s[list(some)].numpy(), M)
+    np.testing.assert_array_equal(got[1][list(some)], ref[1])
+    np.testing.assert_array_equal(got[2][list(some)], ref[2])
+
+
 def test_select_few_tokens_left(cuda_device):
     """Fewer continuations than picks: the rest say so."""
     x, s = draw(1, 2, 5000, "f32", 7)
