@@ -32,10 +32,10 @@ struct RevLayout {
     static constexpr int TI = F32 ? 3 : 1, TP = 3;
     static constexpr int KB = TI * C * NN * 2, YB = TI * C * RW * 32;
     static constexpr int kK = 0, kQ = KB, kY = 2 * KB, kW = kY + YB, kP = kW + 3 * kTri, kS = kP + TP * kTri;
-    static constexpr int stage = (kS + int(sizeof(Scalars)) + 127) / 128 * 128;
+    static constexpr int stage = (kS + int(sizeof(Scalars)) + 255) / 256 * 256;
     static constexpr int stages = F32 ? (NN == 64 ? 4 : 3) : (NN == 64 && GROUPS == 2 ? 5 : 6);
     static constexpr int total = stages * stage + GROUPS * int(sizeof(PrepScratch));
-    static constexpr int threads = RW * 32 + GROUPS * kGroup, meet = RW * 32 + kGroup;
+    static constexpr int meet = RW * 32 + kGroup;
 };
 
 template <int NN, int RW, bool F32, int GROUPS>
@@ -43,7 +43,7 @@ __device__ __forceinline__ void reverse_sweep(const DeltaArgs &p, unsigned block
     using L = RevLayout<NN, RW, F32, GROUPS>;
     using Tin = std::conditional_t<F32, float, __nv_bfloat16>;
     constexpr int TI = L::TI, NB = NN * 2, TB = C * NB, YNB = RW * 32, YTB = C * YNB;
-    extern __shared__ __align__(128) unsigned char sm[];
+    extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t base = smem_addr(sm);
     constexpr int slices = NN / (16 * RW);
     const unsigned unit = block / slices;
@@ -330,9 +330,11 @@ struct GradLayout {
 };
 struct GradScalars {
     float ghi[GC], glo[GC], rk[GC], sq[GC], beta[GC], kin[GC], qin[GC], kout[GC], out[GC];
+    float up[GC], down[GC];         // near: D_ij = up_i down_j
     float row[4][GC], tail[4][GC], col[4][GC], diag[GC], dq[4][GC], dk[4][GC];
     float ss[GT / 32];
     float whole;
+    int near;                       // the chunk's sums of log decays stay within 30 of the middle one
 };
 
 // `rows` rows of W elements (rows from n on as zeros) from an array of the inputs' type (bf16: asynchronous) into
@@ -396,18 +398,42 @@ __device__ __forceinline__ float col_sum(float x) {         // over the eight ro
     return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
-// Elements (r, 2 words of columns c, c + 1) of a tile of TI terms.
+// Two tiles' worth (16 columns from 16 ks on) of elements at the accumulators' places, rows m0 + gr and + 8:
+// v[tile][row half], summed over the terms.
 template <int NB, int TI>
-__device__ __forceinline__ float2 pair_at(uint32_t base, int term, int r, int c) {
-    float2 v = make_float2(0.f, 0.f);
+__device__ __forceinline__ void pairs_at(float2 (&v)[2][2], uint32_t base, int term, int m0, int ks) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) v[t][r] = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = TI - 1; i >= 0; --i) {
-        uint32_t u;
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(u) : "r"(base + i * term + tile<NB>(r, c >> 3) + ((c & 7) << 1)));
-        v.x += lo_f(u);
-        v.y += hi_f(u);
+        uint32_t u[4];
+        ldsm4(u, addr_a<NB>(base + i * term, m0, ks));
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                v[t][r].x += lo_f(u[2 * t + r]);
+                v[t][r].y += hi_f(u[2 * t + r]);
+            }
     }
-    return v;
+}
+// Eight elements of T terms, `term` bytes apart, from 16 bytes of each.
+template <int T>
+__device__ __forceinline__ void eight_at(float (&x)[8], uint32_t at, int term) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+#pragma unroll
+    for (int i = T - 1; i >= 0; --i) {
+        uint32_t u[4];
+        ld_v4(u, at + i * term);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[2 * e] += lo_f(u[e]);
+            x[2 * e + 1] += hi_f(u[e]);
+        }
+    }
 }
 
 template <int NN, bool F32>
@@ -415,7 +441,7 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p) {
     using L = GradLayout<NN, F32>;
     using Tin = std::conditional_t<F32, float, __nv_bfloat16>;
     constexpr int TI = L::TI, TE = L::TE, DW = L::DW, NB = NN * 2, YNB = DW * 2, CT = NN / 32, CW = NN / 4;
-    extern __shared__ __align__(128) unsigned char sm[];
+    extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t base = smem_addr(sm);
     GradScalars *sc = reinterpret_cast<GradScalars *>(sm + L::kF);
     const int hk = blockIdx.x % unsigned(p.Hk);
@@ -448,7 +474,7 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p) {
     float DQ[CT][4] = {}, DK[CT][4] = {};
     for (int hg = 0; hg < group; ++hg) {
         const int h = hk * group + hg;
-        float A[2][4] = {}, B[2][4] = {}, aq[CT][4] = {}, ak[CT][4] = {}, ao[CT][4] = {};
+        float A[2][4] = {}, B[2][4] = {}, QK[2][4] = {}, KK[2][4] = {}, aq[CT][4] = {}, ak[CT][4] = {}, ao[CT][4] = {};
         float ss = 0.f;
         for (int sl = 0; sl < NN / DW; ++sl) {
             const long long ye = t0 * p.H * NN + (long long)h * NN + sl * DW, ys = (long long)p.H * NN;
@@ -466,22 +492,41 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p) {
             load_rows<NN, F32>(base + L::kS, static_cast<const Tin *>(p.keep_S) + se, NN, DW, DW, L::SB);
             load_rows<NN, F32>(base + L::kD, static_cast<const Tin *>(p.keep_dS) + se, NN, DW, DW, L::SB);
             cp_commit();
-            cp_wait<0>();
-            __syncthreads();
-            if (sl == 0) {
+            if (sl == 0) {              // what needs only keys, queries and gates, while the slice is on its way
                 if (hg == 0) {          // lengths: four threads per row, keys then queries
+                    cp_wait<1>();
+                    __syncthreads();
                     const int row = (tid >> 2) & 63, part = tid & 3;
                     const uint32_t at = base + (tid < 256 ? L::kK : L::kQ);
                     float l = 0.f;
-#pragma unroll 4
-                    for (int c = 0; c < NN / 8; ++c) {
-                        const float2 v = pair_at<NB, TI>(at, L::KB, row, 8 * c + 2 * part);
-                        l = fmaf(v.x, v.x, fmaf(v.y, v.y, l));
+#pragma unroll
+                    for (int c = 0; c < NN / 32; ++c) {
+                        float x[8];
+                        eight_at<TI>(x, at + tile<NB>(row, part * (NN / 32) + c), L::KB);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) l = fmaf(x[e], x[e], l);
                     }
                     l = quad_sum(l);
                     l = p.qk_norm ? rsqrtf(l + p.norm_eps) : 1.f;
                     if (part == 0) (tid < 256 ? sc->rk : sc->sq)[row] = tid < 256 ? l : l * p.scale;
                     __syncthreads();
+                }
+                // the keys' and queries' products
+                if (wc <= wr) {
+#pragma unroll
+                    for (int pass = 0; pass < (F32 ? 2 : 1); ++pass)
+#pragma unroll 1
+                        for (int ks = 0; ks < NN / 16; ++ks) {
+                            uint32_t a[TI][4], d[TI][4], b[TI][1][4];
+#pragma unroll
+                            for (int i = 0; i < TI; ++i) {
+                                ldsm4(a[i], addr_a<NB>(base + L::kQ + i * L::KB, 16 * wr, ks));
+                                ldsm4(d[i], addr_a<NB>(base + L::kK + i * L::KB, 16 * wr, ks));
+                                ldsm4(b[i][0], addr_b<NB>(base + L::kK + i * L::KB, j0, ks));
+                            }
+                            mma_terms<TI, TI, 2>(QK, a, b, F32 ? pass : -1);
+                            mma_terms<TI, TI, 2>(KK, d, b, F32 ? pass : -1);
+                        }
                 }
                 if (warp == 0) {        // the decays: two tokens per lane
                     float g[2], b[2];
@@ -504,7 +549,9 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p) {
                         if (lane >= o) G[1] += x;
                     }
                     G[0] = G[1] - second;
-                    const long long last = __shfl_sync(0xffffffffu, G[1], 31);
+                    const long long last = __shfl_sync(0xffffffffu, G[1], 31), mid = __shfl_sync(0xffffffffu, G[1], 15);
+                    const bool near = !nan && __all_sync(0xffffffffu, llabs(G[0] - mid) < (30ll << 32) && llabs(G[1] - mid) < (30ll << 32));
+                    if (lane == 0) sc->near = near;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int i = 2 * lane + e;
@@ -519,9 +566,17 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p) {
                         sc->kout[i] = to * sc->rk[i];
                         sc->out[i] = to * sc->rk[i] * b[e];
                         if (i == GC - 1) sc->whole = in;
+                        // exp(G_i - mid) and its inverse: the high part's exponential, the low part's to second order
+                        const long long off = near ? G[e] - mid : 0;
+                        const float hi = float(int(off >> 22)) * 9.765625e-4f, lo = float(int(off & 0x3fffff)) * 2.3283064365386963e-10f;
+                        const float up = expf(hi), down = expf(-hi), l2 = 0.5f * lo * lo;
+                        sc->up[i] = fmaf(up, lo + l2, up);
+                        sc->down[i] = fmaf(down, l2 - lo, down);
                     }
                 }
             }
+            cp_wait<0>();
+            __syncthreads();
             // A, B over the value channels; dY S, dX S, E dS'. fp32: the slice's sums on their own, small products
             // first (the tensor cores cut as they add, see Acc), then added to the others.
             float tA[2][4] = {}, tB[2][4] = {}, tq[CT][4] = {}, tk[CT][4] = {}, to[CT][4] = {};
@@ -568,63 +623,66 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p) {
                 add_to(ak, tk);
                 add_to(ao, to);
             }
-            for (int i = tid; i < DW * NN / 2; i += GT) {       // <S, dS'>
-                const float2 a = pair_at<NB, TE>(base + L::kS, L::SB, i / (NN / 2), 2 * (i % (NN / 2)));
-                const float2 b = pair_at<NB, TE>(base + L::kD, L::SB, i / (NN / 2), 2 * (i % (NN / 2)));
-                ss = fmaf(a.x, b.x, fmaf(a.y, b.y, ss));
+#pragma unroll
+            for (int i = tid; i < DW * NN / 8; i += GT) {       // <S, dS'>: both tiles have one layout
+                float a[8], b[8];
+                eight_at<TE>(a, base + L::kS + i * 16, L::SB);
+                eight_at<TE>(b, base + L::kD + i * 16, L::SB);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss = fmaf(a[e], b[e], ss);
             }
-        }
-        // the keys' and queries' products
-        float QK[2][4] = {}, KK[2][4] = {};
-        if (wc <= wr) {
-#pragma unroll
-            for (int pass = 0; pass < (F32 ? 2 : 1); ++pass)
-#pragma unroll 1
-                for (int ks = 0; ks < NN / 16; ++ks) {
-                    uint32_t a[TI][4], d[TI][4], b[TI][1][4];
-#pragma unroll
-                    for (int i = 0; i < TI; ++i) {
-                        ldsm4(a[i], addr_a<NB>(base + L::kQ + i * L::KB, 16 * wr, ks));
-                        ldsm4(d[i], addr_a<NB>(base + L::kK + i * L::KB, 16 * wr, ks));
-                        ldsm4(b[i][0], addr_b<NB>(base + L::kK + i * L::KB, j0, ks));
-                    }
-                    mma_terms<TI, TI, 2>(QK, a, b, F32 ? pass : -1);
-                    mma_terms<TI, TI, 2>(KK, d, b, F32 ? pass : -1);
-                }
         }
         __syncthreads();                // the slice has been read, the scalars are there
         // rows i = 16 wr + gr (+ 8), columns j = j0 + 8 m + 2 tc (+ 1)
         float rows[2] = {}, tails[2] = {};
+        const bool near = sc->near != 0;
+        float rn[2], ro[2], rh[2], rl[2];           // rows: factors of n and o, the sums of log decays
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = 16 * wr + gr + 8 * e;
+            const float f = near ? sc->up[i] : 1.f;
+            rn[e] = f * sc->sq[i];
+            ro[e] = f * sc->rk[i];
+            rh[e] = sc->ghi[i];
+            rl[e] = sc->glo[i];
+        }
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             const int j = j0 + 8 * m + 2 * tc;
-            float cols[2] = {};
+            float cols[2] = {}, cf[2], ch[2], cl[2], bt[2];
 #pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-                const int i = 16 * wr + gr + 4 * e;
+            for (int f = 0; f < 2; ++f) {
+                cf[f] = (near ? sc->down[j + f] : 1.f) * sc->rk[j + f];
+                ch[f] = sc->ghi[j + f];
+                cl[f] = sc->glo[j + f];
+                bt[f] = sc->beta[j + f];
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 16 * wr + gr + 8 * e;
                 float vn[2], vo[2];
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
-                    const float d = fast_exp((sc->ghi[i] - sc->ghi[j + f]) + (sc->glo[i] - sc->glo[j + f])) * sc->rk[j + f];
-                    const float nn = j + f <= i ? A[m][e + f] * d * sc->sq[i] : 0.f, oo = j + f < i ? B[m][e + f] * d * sc->rk[i] : 0.f;
-                    const float z = nn * QK[m][e + f] - oo * KK[m][e + f], bt = sc->beta[j + f];
+                    const float d = near ? cf[f] : cf[f] * fast_exp((rh[e] - ch[f]) + (rl[e] - cl[f]));
+                    const float nn = j + f <= i ? A[m][2 * e + f] * d * rn[e] : 0.f, oo = j + f < i ? B[m][2 * e + f] * d * ro[e] : 0.f;
+                    const float z = nn * QK[m][2 * e + f] - oo * KK[m][2 * e + f];
                     if (j + f == i) {       // z_ii belongs to beta alone: g_i changes neither side of it
                         sc->diag[i] = z;
                     } else {
                         cols[f] += z;
-                        rows[e >> 1] = fmaf(bt, z, rows[e >> 1]);
+                        rows[e] = fmaf(bt[f], z, rows[e]);
                     }
-                    vn[f] = nn * bt;
-                    vo[f] = -oo * bt;
+                    vn[f] = nn * bt[f];
+                    vo[f] = -oo * bt[f];
                 }
                 uint32_t a[TE], b[TE];
                 split2<TE>(vn[0], vn[1], a);
                 split2<TE>(vo[0], vo[1], b);
+                const uint32_t to = base + tile<GC * 2>(i, j >> 3) + ((j & 7) << 1);
 #pragma unroll
                 for (int z = 0; z < TE; ++z) {
-                    const uint32_t to = base + z * L::MB + tile<GC * 2>(i, j >> 3) + ((j & 7) << 1);
-                    st_b32(to + L::kN, a[z]);
-                    st_b32(to + L::kO, b[z]);
+                    st_b32(to + z * L::MB + L::kN, a[z]);
+                    st_b32(to + z * L::MB + L::kO, b[z]);
                 }
             }
 #pragma unroll
@@ -634,21 +692,35 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p) {
             }
         }
         // what came through the states, over this warp's key channels
+        float fq[2], fk[2], fo[2], fb[2];
 #pragma unroll
-        for (int m = 0; m < CT; ++m)
+        for (int e = 0; e < 2; ++e) {
+            const int i = 16 * wr + gr + 8 * e;
+            fq[e] = sc->qin[i];
+            fk[e] = sc->kin[i];
+            fo[e] = sc->kout[i];
+            fb[e] = sc->out[i];
+        }
 #pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-                const int i = 16 * wr + gr + 4 * e, c = c0 + 8 * m + 2 * tc;
-                const float2 qv = pair_at<NB, TI>(base + L::kQ, L::KB, i, c), kv = pair_at<NB, TI>(base + L::kK, L::KB, i, c);
-                const float qin = sc->qin[i], kin = sc->kin[i], ko = sc->kout[i], ou = sc->out[i];
-                const float q0 = qin * aq[m][e], q1 = qin * aq[m][e + 1], k0 = kin * ak[m][e], k1 = kin * ak[m][e + 1];
-                rows[e >> 1] += fmaf(qv.x, q0, qv.y * q1) - fmaf(kv.x, k0, kv.y * k1);
-                tails[e >> 1] += ko * fmaf(kv.x, ao[m][e], kv.y * ao[m][e + 1]);
-                DQ[m][e] += q0;
-                DQ[m][e + 1] += q1;
-                DK[m][e] += fmaf(ou, ao[m][e], -k0);
-                DK[m][e + 1] += fmaf(ou, ao[m][e + 1], -k1);
-            }
+        for (int t = 0; t < CT / 2; ++t) {
+            float2 qv[2][2], kv[2][2];
+            pairs_at<NB, TI>(qv, base + L::kQ, L::KB, 16 * wr, c0 / 16 + t);
+            pairs_at<NB, TI>(kv, base + L::kK, L::KB, 16 * wr, c0 / 16 + t);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int m = 2 * t + u;
+                    const float q0 = fq[e] * aq[m][2 * e], q1 = fq[e] * aq[m][2 * e + 1];
+                    const float k0 = fk[e] * ak[m][2 * e], k1 = fk[e] * ak[m][2 * e + 1], o0 = ao[m][2 * e], o1 = ao[m][2 * e + 1];
+                    rows[e] += fmaf(qv[u][e].x, q0, qv[u][e].y * q1) - fmaf(kv[u][e].x, k0, kv[u][e].y * k1);
+                    tails[e] += fo[e] * fmaf(kv[u][e].x, o0, kv[u][e].y * o1);
+                    DQ[m][2 * e] += q0;
+                    DQ[m][2 * e + 1] += q1;
+                    DK[m][2 * e] += fmaf(fb[e], o0, -k0);
+                    DK[m][2 * e + 1] += fmaf(fb[e], o1, -k1);
+                }
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const float x = quad_sum(rows[e]), y = quad_sum(tails[e]);
@@ -753,14 +825,18 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p) {
     if (p.qk_norm) {
         float dq[2] = {}, dk[2] = {};
 #pragma unroll
-        for (int m = 0; m < CT; ++m)
+        for (int t = 0; t < CT / 2; ++t) {
+            float2 qv[2][2], kv[2][2];
+            pairs_at<NB, TI>(qv, base + L::kQ, L::KB, 16 * wr, c0 / 16 + t);
+            pairs_at<NB, TI>(kv, base + L::kK, L::KB, 16 * wr, c0 / 16 + t);
 #pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-                const int i = 16 * wr + gr + 4 * e, c = c0 + 8 * m + 2 * tc;
-                const float2 qv = pair_at<NB, TI>(base + L::kQ, L::KB, i, c), kv = pair_at<NB, TI>(base + L::kK, L::KB, i, c);
-                dq[e >> 1] += fmaf(qv.x, DQ[m][e], qv.y * DQ[m][e + 1]);
-                dk[e >> 1] += fmaf(kv.x, DK[m][e], kv.y * DK[m][e + 1]);
-            }
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    dq[e] += fmaf(qv[u][e].x, DQ[2 * t + u][2 * e], qv[u][e].y * DQ[2 * t + u][2 * e + 1]);
+                    dk[e] += fmaf(kv[u][e].x, DK[2 * t + u][2 * e], kv[u][e].y * DK[2 * t + u][2 * e + 1]);
+                }
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const float x = quad_sum(dq[e]), y = quad_sum(dk[e]);
@@ -770,20 +846,30 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p) {
             }
         }
         __syncthreads();
+        float fq[2], fk[2];
 #pragma unroll
-        for (int m = 0; m < CT; ++m)
+        for (int e = 0; e < 2; ++e) {
+            const int i = 16 * wr + gr + 8 * e;
+            const float rq = sc->sq[i] / p.scale, rk = sc->rk[i];
+            fq[e] = rq * rq * ((sc->dq[0][i] + sc->dq[1][i]) + (sc->dq[2][i] + sc->dq[3][i]));
+            fk[e] = rk * rk * ((sc->dk[0][i] + sc->dk[1][i]) + (sc->dk[2][i] + sc->dk[3][i]));
+        }
 #pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-                const int i = 16 * wr + gr + 4 * e, c = c0 + 8 * m + 2 * tc;
-                const float2 qv = pair_at<NB, TI>(base + L::kQ, L::KB, i, c), kv = pair_at<NB, TI>(base + L::kK, L::KB, i, c);
-                const float rq = sc->sq[i] / p.scale, rk = sc->rk[i];
-                const float fq = rq * rq * ((sc->dq[0][i] + sc->dq[1][i]) + (sc->dq[2][i] + sc->dq[3][i]));
-                const float fk = rk * rk * ((sc->dk[0][i] + sc->dk[1][i]) + (sc->dk[2][i] + sc->dk[3][i]));
-                DQ[m][e] = fmaf(-fq, qv.x, DQ[m][e]);
-                DQ[m][e + 1] = fmaf(-fq, qv.y, DQ[m][e + 1]);
-                DK[m][e] = fmaf(-fk, kv.x, DK[m][e]);
-                DK[m][e + 1] = fmaf(-fk, kv.y, DK[m][e + 1]);
-            }
+        for (int t = 0; t < CT / 2; ++t) {
+            float2 qv[2][2], kv[2][2];
+            pairs_at<NB, TI>(qv, base + L::kQ, L::KB, 16 * wr, c0 / 16 + t);
+            pairs_at<NB, TI>(kv, base + L::kK, L::KB, 16 * wr, c0 / 16 + t);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int m = 2 * t + u;
+                    DQ[m][2 * e] = fmaf(-fq[e], qv[u][e].x, DQ[m][2 * e]);
+                    DQ[m][2 * e + 1] = fmaf(-fq[e], qv[u][e].y, DQ[m][2 * e + 1]);
+                    DK[m][2 * e] = fmaf(-fk[e], kv[u][e].x, DK[m][2 * e]);
+                    DK[m][2 * e + 1] = fmaf(-fk[e], kv[u][e].y, DK[m][2 * e + 1]);
+                }
+        }
     }
 #pragma unroll
     for (int m = 0; m < CT; ++m)

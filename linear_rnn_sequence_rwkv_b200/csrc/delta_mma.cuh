@@ -145,21 +145,23 @@ template <int NB> __device__ __forceinline__ uint32_t tile(int r, int c) {
 // The same inside a 16 x 16 block of bf16 (rows of 32 bytes).
 __device__ __forceinline__ uint32_t block(int r, int c) { return uint32_t(r * 32 + ((c ^ ((r >> 2) & 1)) << 4)); }
 
+// The addresses below step through a row's chunks by an exclusive or on the whole address: tiles start at
+// multiples of 256 bytes, and a lane's first chunk differs from the next ones in the chunk's bits alone.
 // Right operand from a tile that holds it by columns (rows n0 .. n0 + 15 are columns of the operand),
 // depth 16 ks ..: r[0], r[1] for the first eight columns, r[2], r[3] for the next.
 template <int NB> __device__ __forceinline__ uint32_t addr_b(uint32_t base, int n0, int ks) {
     const int l = threadIdx.x & 31;
-    return base + tile<NB>(n0 + (l & 7) + ((l >> 4) << 3), 2 * ks + ((l >> 3) & 1));
+    return (base + n0 * NB + tile<NB>((l & 7) + ((l >> 4) << 3), (l >> 3) & 1)) ^ (ks << 5);
 }
-// Right operand from a tile that holds it by rows (depth k0 ..), columns 8 c ..; for ldsm4t.
+// Right operand from a tile that holds it by rows (depth k0 ..), columns 8 c .. (c even); for ldsm4t.
 template <int NB> __device__ __forceinline__ uint32_t addr_bt(uint32_t base, int k0, int c) {
     const int l = threadIdx.x & 31;
-    return base + tile<NB>(k0 + (l & 7) + (((l >> 3) & 1) << 3), c + (l >> 4));
+    return (base + k0 * NB + tile<NB>((l & 7) + (((l >> 3) & 1) << 3), l >> 4)) ^ (c << 4);
 }
 // Left operand from a tile by rows m0 .., depth 16 ks ..
 template <int NB> __device__ __forceinline__ uint32_t addr_a(uint32_t base, int m0, int ks) {
     const int l = threadIdx.x & 31;
-    return base + tile<NB>(m0 + (l & 7) + (((l >> 3) & 1) << 3), 2 * ks + (l >> 4));
+    return (base + m0 * NB + tile<NB>((l & 7) + (((l >> 3) & 1) << 3), l >> 4)) ^ (ks << 5);
 }
 __device__ __forceinline__ uint32_t addr_block(uint32_t base) {      // by columns, as addr_b
     const int l = threadIdx.x & 31;

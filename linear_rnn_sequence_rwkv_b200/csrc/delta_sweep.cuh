@@ -26,7 +26,7 @@ struct Layout {
     static constexpr int KB = TI * C * NN * 2;              // keys (and as much for queries)
     static constexpr int VB = F32 ? 0 : C * RW * 32;        // values of the CTA's rows; y on its way out
     static constexpr int kK = 0, kQ = KB, kV = STATES ? KB : 2 * KB, kW = kV + VB, kP = kW + 3 * kTri, kS = kP + TP * kTri;
-    static constexpr int stage = (kS + int(sizeof(Scalars)) + 127) / 128 * 128;
+    static constexpr int stage = (kS + int(sizeof(Scalars)) + 255) / 256 * 256;
     // GROUPS chunks being prepared, one at work, and the rest loading: what two CTAs of N = 64 bf16 with two
     // groups, or one of the others, have room (and named barriers) for
     static constexpr int stages = F32 ? (NN == 64 ? 6 : 3) : (NN == 64 && GROUPS == 2 ? 5 : 6);
@@ -73,7 +73,7 @@ __device__ __forceinline__ void forward_sweep(const DeltaArgs &p, unsigned block
     using L = Layout<NN, RW, F32, STATES, GROUPS>;
     using Tin = std::conditional_t<F32, float, __nv_bfloat16>;
     constexpr int TI = L::TI, TP = L::TP, TS = F32 ? 3 : 2, NB = NN * 2, TB = C * NB, VNB = RW * 32;
-    extern __shared__ __align__(128) unsigned char sm[];
+    extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t base = smem_addr(sm);
     constexpr int slices = NN / (16 * RW);
     const unsigned unit = block / slices;
