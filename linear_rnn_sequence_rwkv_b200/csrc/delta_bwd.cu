@@ -337,33 +337,48 @@ struct GradScalars {
     int near;                       // the chunk's sums of log decays stay within 30 of the middle one
 };
 
-// `rows` rows of W elements (rows from n on as zeros) from an array of the inputs' type (bf16: asynchronous) into
-// tiles of bf16 terms (fp32: three, TERM bytes apart).
-template <int W, bool F32>
-__device__ __forceinline__ void load_rows(uint32_t dst, const void *src, long long stride, int rows, int n, int term) {
-    for (int i = threadIdx.x; i < rows * (W / 8); i += GT) {
-        const int r = i / (W / 8), c = i % (W / 8);
-        const uint32_t to = dst + tile<W * 2>(r, c);
-        if constexpr (!F32) {
-            const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(src);
-            cp16(to, r < n ? p + r * stride + 8 * c : p, r < n);
-        } else {
-            float4 x = make_float4(0, 0, 0, 0), y = x;
-            if (r < n) {
-                const float *p = static_cast<const float *>(src) + r * stride + 8 * c;
-                x = *reinterpret_cast<const float4 *>(p);
-                y = *reinterpret_cast<const float4 *>(p + 4);
-            }
-            uint32_t w[4][3];
-            split2<3>(x.x, x.y, w[0]);
-            split2<3>(x.z, x.w, w[1]);
-            split2<3>(y.x, y.y, w[2]);
-            split2<3>(y.z, y.w, w[3]);
+// Where a thread's pieces of a tile of ROWS rows of W elements lie: piece i is row r + i STEP, column chunk c.
+template <int W, int ROWS>
+struct Pieces {
+    static constexpr int STEP = GT / (W / 8), N = (ROWS + STEP - 1) / STEP;
+    int r;
+    uint32_t to;            // of the first piece in the tile
+    long long from, step;   // elements, of rows `stride` apart
+    __device__ __forceinline__ Pieces(long long stride) {
+        r = threadIdx.x / (W / 8);
+        to = tile<W * 2>(r, threadIdx.x % (W / 8));
+        from = r * stride + 8 * (threadIdx.x % (W / 8));
+        step = STEP * stride;
+    }
+    // From an array of the inputs' type into a tile (rows from n on as zeros): bf16 asynchronously; fp32 as three
+    // terms `term` bytes apart.
+    template <bool F32>
+    __device__ __forceinline__ void load(uint32_t dst, const void *src, int n, int term) const {
+        const char *p = static_cast<const char *>(src) + from * (F32 ? 4 : 2);
 #pragma unroll
-            for (int k = 0; k < 3; ++k) st_v4(to + k * term, w[0][k], w[1][k], w[2][k], w[3][k]);
+        for (int i = 0; i < N; ++i) {
+            if (ROWS % STEP && r + i * STEP >= ROWS) break;
+            const bool there = r + i * STEP < n;
+            const uint32_t at = dst + to + i * STEP * W * 2;        // eight rows or more on: the same place in the swizzle
+            if constexpr (!F32) {
+                cp16(at, there ? p + i * step * 2 : static_cast<const char *>(src), there);
+            } else {
+                float4 x = make_float4(0, 0, 0, 0), y = x;
+                if (there) {
+                    x = *reinterpret_cast<const float4 *>(p + i * step * 4);
+                    y = *reinterpret_cast<const float4 *>(p + i * step * 4 + 16);
+                }
+                uint32_t w[4][3];
+                split2<3>(x.x, x.y, w[0]);
+                split2<3>(x.z, x.w, w[1]);
+                split2<3>(y.x, y.y, w[2]);
+                split2<3>(y.z, y.w, w[3]);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) st_v4(at + k * term, w[0][k], w[1][k], w[2][k], w[3][k]);
+            }
         }
     }
-}
+};
 
 // d[0 .. CT) += a b over the pairs of terms that count: a TA terms of a left operand, b TB terms of right operands
 // of 16 columns each. top: 1 only the leading pair, 0 only the others, -1 all.
@@ -468,29 +483,30 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p) {
     const int wr = warp & 3, wc = warp >> 2, c0 = wc * CW, j0 = wc * 16;   // rows 16 wr; key channels c0; tokens j0 ..
     const int group = p.H / p.Hk;
 
-    load_rows<NN, F32>(base + L::kK, static_cast<const Tin *>(p.k) + t0 * p.ks + hk * NN, p.ks, GC, n, L::KB);
-    load_rows<NN, F32>(base + L::kQ, static_cast<const Tin *>(p.q) + t0 * p.qs + hk * NN, p.qs, GC, n, L::KB);
+    Pieces<NN, GC>(p.ks).template load<F32>(base + L::kK, static_cast<const Tin *>(p.k) + t0 * p.ks + hk * NN, n, L::KB);
+    Pieces<NN, GC>(p.qs).template load<F32>(base + L::kQ, static_cast<const Tin *>(p.q) + t0 * p.qs + hk * NN, n, L::KB);
     cp_commit();
+    const Pieces<DW, GC> tok((long long)p.H * NN);
+    const Pieces<NN, DW> sta(NN);
     float DQ[CT][4] = {}, DK[CT][4] = {};
     for (int hg = 0; hg < group; ++hg) {
         const int h = hk * group + hg;
         float A[2][4] = {}, B[2][4] = {}, QK[2][4] = {}, KK[2][4] = {}, aq[CT][4] = {}, ak[CT][4] = {}, ao[CT][4] = {};
         float ss = 0.f;
         for (int sl = 0; sl < NN / DW; ++sl) {
-            const long long ye = t0 * p.H * NN + (long long)h * NN + sl * DW, ys = (long long)p.H * NN;
-            const long long se = ((slot * p.H + h) * NN + sl * DW) * NN;
+            const long long ye = t0 * p.H * NN + (long long)h * NN + sl * DW, se = ((slot * p.H + h) * NN + sl * DW) * NN;
             __syncthreads();            // the last readers of what lies there
-            load_rows<DW, F32>(base + L::kY, static_cast<const Tin *>(p.dy) + ye, ys, GC, n, L::YB);
-            load_rows<DW, F32>(base + L::kE, static_cast<const Tin *>(p.keep_E) + ye, ys, GC, n, L::YB);
-            load_rows<DW, F32>(base + L::kX, static_cast<const Tin *>(p.dv) + ye, ys, GC, n, L::YB);
-            if constexpr (!F32) {
-                load_rows<DW, F32>(base + L::kE + L::YB, static_cast<const Tin *>(p.keep_E) + p.keep_lo + ye, ys, GC, n, L::YB);
-                load_rows<DW, F32>(base + L::kX + L::YB, static_cast<const Tin *>(p.keep_dlo) + ye, ys, GC, n, L::YB);
-                load_rows<NN, F32>(base + L::kS + L::SB, static_cast<const Tin *>(p.keep_S) + p.keep_second + se, NN, DW, DW, L::SB);
-                load_rows<NN, F32>(base + L::kD + L::SB, static_cast<const Tin *>(p.keep_dS) + p.keep_second + se, NN, DW, DW, L::SB);
+            tok.template load<F32>(base + L::kY, static_cast<const Tin *>(p.dy) + ye, n, L::YB);
+            tok.template load<F32>(base + L::kE, static_cast<const Tin *>(p.keep_E) + ye, n, L::YB);
+            tok.template load<F32>(base + L::kX, static_cast<const Tin *>(p.dv) + ye, n, L::YB);
+            sta.template load<F32>(base + L::kS, static_cast<const Tin *>(p.keep_S) + se, DW, L::SB);
+            sta.template load<F32>(base + L::kD, static_cast<const Tin *>(p.keep_dS) + se, DW, L::SB);
+            if constexpr (!F32) {       // the second terms
+                tok.template load<F32>(base + L::kE + L::YB, static_cast<const Tin *>(p.keep_E) + p.keep_lo + ye, n, L::YB);
+                tok.template load<F32>(base + L::kX + L::YB, static_cast<const Tin *>(p.keep_dlo) + ye, n, L::YB);
+                sta.template load<F32>(base + L::kS + L::SB, static_cast<const Tin *>(p.keep_S) + p.keep_second + se, DW, L::SB);
+                sta.template load<F32>(base + L::kD + L::SB, static_cast<const Tin *>(p.keep_dS) + p.keep_second + se, DW, L::SB);
             }
-            load_rows<NN, F32>(base + L::kS, static_cast<const Tin *>(p.keep_S) + se, NN, DW, DW, L::SB);
-            load_rows<NN, F32>(base + L::kD, static_cast<const Tin *>(p.keep_dS) + se, NN, DW, DW, L::SB);
             cp_commit();
             if (sl == 0) {              // what needs only keys, queries and gates, while the slice is on its way
                 if (hg == 0) {          // lengths: four threads per row, keys then queries
