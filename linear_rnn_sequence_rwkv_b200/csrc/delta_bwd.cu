@@ -21,6 +21,8 @@
 // difference of large sums and would show a single term's rounding several times over.
 #include "delta_sweep.cuh"
 
+#include <algorithm>
+
 namespace wkv7 {
 
 using namespace dm;
@@ -318,15 +320,10 @@ __global__ void __launch_bounds__(RW * 32 + GROUPS * kGroup, (!F32 && NN == 64 &
 
 constexpr int GC = 64, GT = 512;        // tokens, threads (16 warps: 4 row blocks of 16 by 4 column groups)
 
-template <int NN, bool F32>
-struct GradLayout {
-    static constexpr int TI = F32 ? 3 : 1, TE = F32 ? 3 : 2, DW = F32 ? 32 : 64;   // DW: value channels at a time
-    static constexpr int KB = GC * NN * 2, YB = GC * DW * 2, SB = DW * NN * 2, MB = GC * GC * 2;   // one term each
-    static constexpr int kK = 0, kQ = TI * KB, kSlice = 2 * TI * KB;
-    static constexpr int kY = kSlice, kE = kY + TI * YB, kX = kE + TE * YB, kS = kX + TE * YB, kD = kS + TE * SB;
-    static constexpr int kN = kSlice, kO = kN + TE * MB;                 // n and -o, where the slice was
-    static constexpr int slice_end = kD + TE * SB, mats_end = kO + TE * MB;
-    static constexpr int kF = slice_end > mats_end ? slice_end : mats_end;
+// Tokens t0 .. t0 + n - 1 of a sequence, number `slot` of all chunks, and a key head. n = 0: none left.
+struct GradChunk {
+    long long t0, slot;
+    int n, hk;
 };
 struct GradScalars {
     float ghi[GC], glo[GC], rk[GC], sq[GC], beta[GC], kin[GC], qin[GC], kout[GC], out[GC];
@@ -335,6 +332,22 @@ struct GradScalars {
     float ss[GT / 32];
     float whole;
     int near;                       // the chunk's sums of log decays stay within 30 of the middle one
+    GradChunk next;
+};
+
+template <int NN, bool F32>
+struct GradLayout {
+    static constexpr int TI = F32 ? 3 : 1, TE = F32 ? 3 : 2, DW = F32 ? 32 : 64;   // DW: value channels at a time
+    static constexpr int KB = GC * NN * 2, YB = GC * DW * 2, SB = DW * NN * 2, MB = GC * GC * 2;   // one term each
+    // Two sets of tiles fit: a CTA per SM stays and loads the next chunk under the products of this one (8 x 1024 tokens
+    // of 12 heads, the whole backward: 258 us against 270 with a CTA per chunk).
+    static constexpr bool AHEAD = NN == 64 && !F32;
+    static constexpr int kK = 0, kQ = TI * KB, kSlice = 2 * TI * KB;
+    static constexpr int kY = kSlice, kE = kY + TI * YB, kX = kE + TE * YB, kS = kX + TE * YB, kD = kS + TE * SB;
+    static constexpr int kN = kSlice, kO = kN + TE * MB;                 // n and -o, where the slice was
+    static constexpr int slice_end = kD + TE * SB, mats_end = kO + TE * MB;
+    static constexpr int kF = slice_end > mats_end ? slice_end : mats_end;
+    static constexpr int total = (AHEAD ? 2 : 1) * kF + int(sizeof(GradScalars));
 };
 
 // Where a thread's pieces of a tile of ROWS rows of W elements lie: piece i is row r + i STEP, column chunk c.
@@ -451,457 +464,506 @@ __device__ __forceinline__ void eight_at(float (&x)[8], uint32_t at, int term) {
     }
 }
 
+// The first task from `task` on that has tokens: task = (chunk number) * Hk + key head.
+__device__ __forceinline__ GradChunk grad_chunk(const DeltaArgs &p, unsigned &task, unsigned tasks) {
+    for (; task < tasks; task += gridDim.x) {
+        const long long slot = task / unsigned(p.Hk);
+        // the sequence of this chunk: the last one that starts at or before it
+        int s = 0;
+        for (int lo = 0, hi = p.B; lo < hi;) {
+            const int mid = (lo + hi) >> 1;
+            const long long first = p.cu ? min(max(p.cu[mid], 0), p.T) : (long long)mid * p.T;
+            if (delta_slot(first, mid) <= slot) {
+                s = mid;
+                lo = mid + 1;
+            } else {
+                hi = mid;
+            }
+        }
+        long long t0, t1;
+        delta_rows(p.cu, p.T, s, t0, t1);
+        const long long chunk = slot - delta_slot(t0, s);
+        t0 += chunk * GC;
+        if (chunk >= 0 && t0 < t1) return {t0, slot, int(min((long long)GC, t1 - t0)), int(task % unsigned(p.Hk))};
+    }
+    return {0, 0, 0, 0};
+}
+
 template <int NN, bool F32>
-__global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p) {
+__global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p, unsigned tasks) {
     using L = GradLayout<NN, F32>;
     using Tin = std::conditional_t<F32, float, __nv_bfloat16>;
     constexpr int TI = L::TI, TE = L::TE, DW = L::DW, NB = NN * 2, YNB = DW * 2, CT = NN / 32, CW = NN / 4;
     extern __shared__ __align__(1024) unsigned char sm[];
-    const uint32_t base = smem_addr(sm);
-    GradScalars *sc = reinterpret_cast<GradScalars *>(sm + L::kF);
-    const int hk = blockIdx.x % unsigned(p.Hk);
-    const long long slot = blockIdx.x / unsigned(p.Hk);
-    // the sequence of this chunk: the last one that starts at or before it
-    int s = 0;
-    for (int lo = 0, hi = p.B; lo < hi;) {
-        const int mid = (lo + hi) >> 1;
-        const long long first = p.cu ? min(max(p.cu[mid], 0), p.T) : (long long)mid * p.T;
-        if (delta_slot(first, mid) <= slot) {
-            s = mid;
-            lo = mid + 1;
-        } else {
-            hi = mid;
-        }
-    }
-    long long t0, t1;
-    delta_rows(p.cu, p.T, s, t0, t1);
-    const long long chunk = slot - delta_slot(t0, s);
-    t0 += chunk * GC;
-    if (chunk < 0 || t0 >= t1) return;
-    const int n = int(min((long long)GC, t1 - t0));
+    GradScalars *sc = reinterpret_cast<GradScalars *>(sm + L::total - sizeof(GradScalars));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tc = lane & 3;
+    constexpr int scalar_warp = 12;     // the one with the fewest products (wr = 0, wc = 3) sees to the gates
     const int wr = warp & 3, wc = warp >> 2, c0 = wc * CW, j0 = wc * 16;   // rows 16 wr; key channels c0; tokens j0 ..
     const int group = p.H / p.Hk;
-
-    Pieces<NN, GC>(p.ks).template load<F32>(base + L::kK, static_cast<const Tin *>(p.k) + t0 * p.ks + hk * NN, n, L::KB);
-    Pieces<NN, GC>(p.qs).template load<F32>(base + L::kQ, static_cast<const Tin *>(p.q) + t0 * p.qs + hk * NN, n, L::KB);
-    cp_commit();
     const Pieces<DW, GC> tok((long long)p.H * NN);
     const Pieces<NN, DW> sta(NN);
-    float DQ[CT][4] = {}, DK[CT][4] = {};
-    for (int hg = 0; hg < group; ++hg) {
-        const int h = hk * group + hg;
-        float A[2][4] = {}, B[2][4] = {}, QK[2][4] = {}, KK[2][4] = {}, aq[CT][4] = {}, ak[CT][4] = {}, ao[CT][4] = {};
-        float ss = 0.f;
-        for (int sl = 0; sl < NN / DW; ++sl) {
-            const long long ye = t0 * p.H * NN + (long long)h * NN + sl * DW, se = ((slot * p.H + h) * NN + sl * DW) * NN;
-            __syncthreads();            // the last readers of what lies there
-            tok.template load<F32>(base + L::kY, static_cast<const Tin *>(p.dy) + ye, n, L::YB);
-            tok.template load<F32>(base + L::kE, static_cast<const Tin *>(p.keep_E) + ye, n, L::YB);
-            tok.template load<F32>(base + L::kX, static_cast<const Tin *>(p.dv) + ye, n, L::YB);
-            sta.template load<F32>(base + L::kS, static_cast<const Tin *>(p.keep_S) + se, DW, L::SB);
-            sta.template load<F32>(base + L::kD, static_cast<const Tin *>(p.keep_dS) + se, DW, L::SB);
-            if constexpr (!F32) {       // the second terms
-                tok.template load<F32>(base + L::kE + L::YB, static_cast<const Tin *>(p.keep_E) + p.keep_lo + ye, n, L::YB);
-                tok.template load<F32>(base + L::kX + L::YB, static_cast<const Tin *>(p.keep_dlo) + ye, n, L::YB);
-                sta.template load<F32>(base + L::kS + L::SB, static_cast<const Tin *>(p.keep_S) + p.keep_second + se, DW, L::SB);
-                sta.template load<F32>(base + L::kD + L::SB, static_cast<const Tin *>(p.keep_dS) + p.keep_second + se, DW, L::SB);
-            }
-            cp_commit();
-            if (sl == 0) {              // what needs only keys, queries and gates, while the slice is on its way
-                if (hg == 0) {          // lengths: four threads per row, keys then queries
-                    cp_wait<1>();
-                    __syncthreads();
-                    const int row = (tid >> 2) & 63, part = tid & 3;
-                    const uint32_t at = base + (tid < 256 ? L::kK : L::kQ);
-                    float l = 0.f;
+    auto load_keys = [&](uint32_t to, const GradChunk &c) {
+        Pieces<NN, GC>(p.ks).template load<F32>(to + L::kK, static_cast<const Tin *>(p.k) + c.t0 * p.ks + c.hk * NN, c.n, L::KB);
+        Pieces<NN, GC>(p.qs).template load<F32>(to + L::kQ, static_cast<const Tin *>(p.q) + c.t0 * p.qs + c.hk * NN, c.n, L::KB);
+    };
+    auto load_slice = [&](uint32_t to, const GradChunk &c, int h, int sl) {
+        const long long ye = c.t0 * p.H * NN + (long long)h * NN + sl * DW, se = ((c.slot * p.H + h) * NN + sl * DW) * NN;
+        tok.template load<F32>(to + L::kY, static_cast<const Tin *>(p.dy) + ye, c.n, L::YB);
+        tok.template load<F32>(to + L::kE, static_cast<const Tin *>(p.keep_E) + ye, c.n, L::YB);
+        tok.template load<F32>(to + L::kX, static_cast<const Tin *>(p.dv) + ye, c.n, L::YB);
+        sta.template load<F32>(to + L::kS, static_cast<const Tin *>(p.keep_S) + se, DW, L::SB);
+        sta.template load<F32>(to + L::kD, static_cast<const Tin *>(p.keep_dS) + se, DW, L::SB);
+        if constexpr (!F32) {           // the second terms
+            tok.template load<F32>(to + L::kE + L::YB, static_cast<const Tin *>(p.keep_E) + p.keep_lo + ye, c.n, L::YB);
+            tok.template load<F32>(to + L::kX + L::YB, static_cast<const Tin *>(p.keep_dlo) + ye, c.n, L::YB);
+            sta.template load<F32>(to + L::kS + L::SB, static_cast<const Tin *>(p.keep_S) + p.keep_second + se, DW, L::SB);
+            sta.template load<F32>(to + L::kD + L::SB, static_cast<const Tin *>(p.keep_dS) + p.keep_second + se, DW, L::SB);
+        }
+    };
+    unsigned at_task = blockIdx.x;
+    GradChunk cur = grad_chunk(p, at_task, tasks);
+    if (cur.n == 0) return;
+    // of the keys and queries, and of the slice: each moves to the other set and back
+    const uint32_t both = 2 * smem_addr(sm) + L::kF;
+    uint32_t keys = smem_addr(sm), base = keys;
+    load_keys(keys, cur);
+    if constexpr (L::AHEAD) load_slice(base, cur, cur.hk * group, 0);
+    cp_commit();
+    while (true) {
+        const long long t0 = cur.t0;
+        const int n = cur.n, hk = cur.hk;
+        float DQ[CT][4] = {}, DK[CT][4] = {};
+        for (int hg = 0; hg < group; ++hg) {
+            const int h = hk * group + hg;
+            float A[2][4] = {}, B[2][4] = {}, QK[2][4] = {}, KK[2][4] = {}, aq[CT][4] = {}, ak[CT][4] = {}, ao[CT][4] = {};
+            float ss = 0.f;
+            for (int sl = 0; sl < NN / DW; ++sl) {
+                [[maybe_unused]] Gate<F32> gates[2];
+                if constexpr (L::AHEAD) cp_wait<0>();
+                __syncthreads();            // the last readers of what lies there
+                if constexpr (L::AHEAD) {
+                    if (warp == scalar_warp) {
 #pragma unroll
-                    for (int c = 0; c < NN / 32; ++c) {
-                        float x[8];
-                        eight_at<TI>(x, at + tile<NB>(row, part * (NN / 32) + c), L::KB);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) l = fmaf(x[e], x[e], l);
+                        for (int e = 0; e < 2; ++e) gates[e].load(p.g, p.beta, (t0 + 2 * lane + e) * p.H + h, 2 * lane + e < n);
                     }
-                    l = quad_sum(l);
-                    l = p.qk_norm ? rsqrtf(l + p.norm_eps) : 1.f;
-                    if (part == 0) (tid < 256 ? sc->rk : sc->sq)[row] = tid < 256 ? l : l * p.scale;
-                    __syncthreads();
-                }
-                // the keys' and queries' products
-                if (wc <= wr) {
-#pragma unroll
-                    for (int pass = 0; pass < (F32 ? 2 : 1); ++pass)
-#pragma unroll 1
-                        for (int ks = 0; ks < NN / 16; ++ks) {
-                            uint32_t a[TI][4], d[TI][4], b[TI][1][4];
-#pragma unroll
-                            for (int i = 0; i < TI; ++i) {
-                                ldsm4(a[i], addr_a<NB>(base + L::kQ + i * L::KB, 16 * wr, ks));
-                                ldsm4(d[i], addr_a<NB>(base + L::kK + i * L::KB, 16 * wr, ks));
-                                ldsm4(b[i][0], addr_b<NB>(base + L::kK + i * L::KB, j0, ks));
-                            }
-                            mma_terms<TI, TI, 2>(QK, a, b, F32 ? pass : -1);
-                            mma_terms<TI, TI, 2>(KK, d, b, F32 ? pass : -1);
+                    if (hg + 1 < group) {
+                        // the keys and queries stay where they are
+                        load_slice(both - base, cur, h + 1, 0);
+                    } else {
+                        const GradChunk next = grad_chunk(p, at_task += gridDim.x, tasks);
+                        if (tid == 0) sc->next = next;
+                        if (next.n) {
+                            load_keys(both - keys, next);
+                            load_slice(both - base, next, next.hk * group, 0);
                         }
+                    }
+                } else {
+                    load_slice(base, cur, h, sl);
                 }
-                if (warp == 0) {        // the decays: two tokens per lane
-                    float g[2], b[2];
-                    long long G[2];
+                cp_commit();
+                if (sl == 0) {              // what needs only keys, queries and gates, while the slice is on its way
+                    if (hg == 0) {          // lengths: four threads per row, keys then queries
+                        if constexpr (!L::AHEAD) {
+                            cp_wait<1>();
+                            __syncthreads();
+                        }
+                        const int row = (tid >> 2) & 63, part = tid & 3;
+                        const uint32_t at = keys + (tid < 256 ? L::kK : L::kQ);
+                        float l = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int i = 2 * lane + e;
-                        Gate<F32> gate;
-                        gate.load(p.g, p.beta, (t0 + i) * p.H + h, i < n);
-                        g[e] = delta_clamp(gate.num(gate.g));
-                        b[e] = gate.num(gate.beta);
-                        G[e] = llrintf(fminf(g[e], 120.f) * 4294967296.f);
+                        for (int c = 0; c < NN / 32; ++c) {
+                            float x[8];
+                            eight_at<TI>(x, at + tile<NB>(row, part * (NN / 32) + c), L::KB);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) l = fmaf(x[e], x[e], l);
+                        }
+                        l = quad_sum(l);
+                        l = p.qk_norm ? rsqrtf(l + p.norm_eps) : 1.f;
+                        if (part == 0) (tid < 256 ? sc->rk : sc->sq)[row] = tid < 256 ? l : l * p.scale;
+                        __syncthreads();
                     }
-                    const bool nan = __any_sync(0xffffffffu, g[0] != g[0] || g[1] != g[1]);
-                    const long long second = G[1];
-                    G[1] += G[0];
+                    // the keys' and queries' products
+                    if (wc <= wr) {
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const long long x = __shfl_up_sync(0xffffffffu, G[1], o);
-                        if (lane >= o) G[1] += x;
-                    }
-                    G[0] = G[1] - second;
-                    const long long last = __shfl_sync(0xffffffffu, G[1], 31), mid = __shfl_sync(0xffffffffu, G[1], 15);
-                    const bool near = !nan && __all_sync(0xffffffffu, llabs(G[0] - mid) < (30ll << 32) && llabs(G[1] - mid) < (30ll << 32));
-                    if (lane == 0) sc->near = near;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int i = 2 * lane + e;
-                        const float bad = nan ? __int_as_float(0x7fffffff) : 0.f;
-                        const float in = expf(float(G[e]) * 2.3283064365386963e-10f) + bad;
-                        const float to = expf(float(last - G[e]) * 2.3283064365386963e-10f);
-                        sc->ghi[i] = float(int(G[e] >> 22)) * 9.765625e-4f + bad;
-                        sc->glo[i] = float(int(G[e] & 0x3fffff)) * 2.3283064365386963e-10f;
-                        sc->beta[i] = b[e];
-                        sc->kin[i] = in * sc->rk[i];
-                        sc->qin[i] = in * sc->sq[i];
-                        sc->kout[i] = to * sc->rk[i];
-                        sc->out[i] = to * sc->rk[i] * b[e];
-                        if (i == GC - 1) sc->whole = in;
-                        // exp(G_i - mid) and its inverse: the high part's exponential, the low part's to second order
-                        const long long off = near ? G[e] - mid : 0;
-                        const float hi = float(int(off >> 22)) * 9.765625e-4f, lo = float(int(off & 0x3fffff)) * 2.3283064365386963e-10f;
-                        const float up = expf(hi), down = expf(-hi), l2 = 0.5f * lo * lo;
-                        sc->up[i] = fmaf(up, lo + l2, up);
-                        sc->down[i] = fmaf(down, l2 - lo, down);
-                    }
-                }
-            }
-            cp_wait<0>();
-            __syncthreads();
-            // A, B over the value channels; dY S, dX S, E dS'. fp32: the slice's sums on their own, small products
-            // first (the tensor cores cut as they add, see Acc), then added to the others.
-            float tA[2][4] = {}, tB[2][4] = {}, tq[CT][4] = {}, tk[CT][4] = {}, to[CT][4] = {};
-            float (&A_)[2][4] = F32 ? tA : A, (&B_)[2][4] = F32 ? tB : B;
-            float (&q_)[CT][4] = F32 ? tq : aq, (&k_)[CT][4] = F32 ? tk : ak, (&o_)[CT][4] = F32 ? to : ao;
-#pragma unroll
-            for (int pass = 0; pass < (F32 ? 2 : 1); ++pass) {
-                const int top = F32 ? pass : -1;
+                        for (int pass = 0; pass < (F32 ? 2 : 1); ++pass)
 #pragma unroll 1
-                for (int ks = 0; ks < DW / 16; ++ks) {
-                    uint32_t y[TI][4], x[TE][4], e[TE][4];
+                            for (int ks = 0; ks < NN / 16; ++ks) {
+                                uint32_t a[TI][4], d[TI][4], b[TI][1][4];
 #pragma unroll
-                    for (int i = 0; i < TI; ++i) ldsm4(y[i], addr_a<YNB>(base + L::kY + i * L::YB, 16 * wr, ks));
-#pragma unroll
-                    for (int i = 0; i < TE; ++i) {
-                        ldsm4(x[i], addr_a<YNB>(base + L::kX + i * L::YB, 16 * wr, ks));
-                        ldsm4(e[i], addr_a<YNB>(base + L::kE + i * L::YB, 16 * wr, ks));
+                                for (int i = 0; i < TI; ++i) {
+                                    ldsm4(a[i], addr_a<NB>(keys + L::kQ + i * L::KB, 16 * wr, ks));
+                                    ldsm4(d[i], addr_a<NB>(keys + L::kK + i * L::KB, 16 * wr, ks));
+                                    ldsm4(b[i][0], addr_b<NB>(keys + L::kK + i * L::KB, j0, ks));
+                                }
+                                mma_terms<TI, TI, 2>(QK, a, b, F32 ? pass : -1);
+                                mma_terms<TI, TI, 2>(KK, d, b, F32 ? pass : -1);
+                            }
                     }
-                    if (wc <= wr) {         // tokens j of this warp's column group are not all behind its rows
-                        uint32_t b[TE][1][4];
+                    if (warp == scalar_warp) {        // the decays: two tokens per lane
+                        float g[2], b[2];
+                        long long G[2];
 #pragma unroll
-                        for (int i = 0; i < TE; ++i) ldsm4(b[i][0], addr_b<YNB>(base + L::kE + i * L::YB, j0, ks));
-                        mma_terms<TI, TE, 2>(A_, y, b, top);
-                        mma_terms<TE, TE, 2>(B_, x, b, top);
+                        for (int e = 0; e < 2; ++e) {
+                            const int i = 2 * lane + e;
+                            if constexpr (!L::AHEAD) gates[e].load(p.g, p.beta, (t0 + i) * p.H + h, i < n);
+                            g[e] = delta_clamp(gates[e].num(gates[e].g));
+                            b[e] = gates[e].num(gates[e].beta);
+                            G[e] = llrintf(fminf(g[e], 120.f) * 4294967296.f);
+                        }
+                        const bool nan = __any_sync(0xffffffffu, g[0] != g[0] || g[1] != g[1]);
+                        const long long second = G[1];
+                        G[1] += G[0];
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const long long x = __shfl_up_sync(0xffffffffu, G[1], o);
+                            if (lane >= o) G[1] += x;
+                        }
+                        G[0] = G[1] - second;
+                        const long long last = __shfl_sync(0xffffffffu, G[1], 31), mid = __shfl_sync(0xffffffffu, G[1], 15);
+                        const bool near = !nan && __all_sync(0xffffffffu, llabs(G[0] - mid) < (30ll << 32) && llabs(G[1] - mid) < (30ll << 32));
+                        if (lane == 0) sc->near = near;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int i = 2 * lane + e;
+                            const float bad = nan ? __int_as_float(0x7fffffff) : 0.f;
+                            const float in = expf(float(G[e]) * 2.3283064365386963e-10f) + bad;
+                            const float to = expf(float(last - G[e]) * 2.3283064365386963e-10f);
+                            sc->ghi[i] = float(int(G[e] >> 22)) * 9.765625e-4f + bad;
+                            sc->glo[i] = float(int(G[e] & 0x3fffff)) * 2.3283064365386963e-10f;
+                            sc->beta[i] = b[e];
+                            sc->kin[i] = in * sc->rk[i];
+                            sc->qin[i] = in * sc->sq[i];
+                            sc->kout[i] = to * sc->rk[i];
+                            sc->out[i] = to * sc->rk[i] * b[e];
+                            if (i == GC - 1) sc->whole = in;
+                            // exp(G_i - mid) and its inverse: the high part's exponential, the low part's to second order
+                            const long long off = near ? G[e] - mid : 0;
+                            const float hi = float(int(off >> 22)) * 9.765625e-4f, lo = float(int(off & 0x3fffff)) * 2.3283064365386963e-10f;
+                            const float up = expf(hi), down = expf(-hi), l2 = 0.5f * lo * lo;
+                            sc->up[i] = fmaf(up, lo + l2, up);
+                            sc->down[i] = fmaf(down, l2 - lo, down);
+                        }
                     }
-                    uint32_t b[TE][CT / 2][4];
+                }
+                if constexpr (!L::AHEAD) {
+                    cp_wait<0>();
+                    __syncthreads();
+                }
+                // A, B over the value channels; dY S, dX S, E dS'. fp32: the slice's sums on their own, small products
+                // first (the tensor cores cut as they add, see Acc), then added to the others.
+                float tA[2][4] = {}, tB[2][4] = {}, tq[CT][4] = {}, tk[CT][4] = {}, to[CT][4] = {};
+                float (&A_)[2][4] = F32 ? tA : A, (&B_)[2][4] = F32 ? tB : B;
+                float (&q_)[CT][4] = F32 ? tq : aq, (&k_)[CT][4] = F32 ? tk : ak, (&o_)[CT][4] = F32 ? to : ao;
 #pragma unroll
-                    for (int i = 0; i < TE; ++i)
+                for (int pass = 0; pass < (F32 ? 2 : 1); ++pass) {
+                    const int top = F32 ? pass : -1;
+#pragma unroll 1
+                    for (int ks = 0; ks < DW / 16; ++ks) {
+                        uint32_t y[TI][4], x[TE][4], e[TE][4];
 #pragma unroll
-                        for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kS + i * L::SB, 16 * ks, c0 / 8 + 2 * m));
-                    mma_terms<TI, TE, CT>(q_, y, b, top);
-                    mma_terms<TE, TE, CT>(k_, x, b, top);
+                        for (int i = 0; i < TI; ++i) ldsm4(y[i], addr_a<YNB>(base + L::kY + i * L::YB, 16 * wr, ks));
 #pragma unroll
-                    for (int i = 0; i < TE; ++i)
+                        for (int i = 0; i < TE; ++i) {
+                            ldsm4(x[i], addr_a<YNB>(base + L::kX + i * L::YB, 16 * wr, ks));
+                            ldsm4(e[i], addr_a<YNB>(base + L::kE + i * L::YB, 16 * wr, ks));
+                        }
+                        if (wc <= wr) {         // tokens j of this warp's column group are not all behind its rows
+                            uint32_t b[TE][1][4];
 #pragma unroll
-                        for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kD + i * L::SB, 16 * ks, c0 / 8 + 2 * m));
-                    mma_terms<TE, TE, CT>(o_, e, b, top);
+                            for (int i = 0; i < TE; ++i) ldsm4(b[i][0], addr_b<YNB>(base + L::kE + i * L::YB, j0, ks));
+                            mma_terms<TI, TE, 2>(A_, y, b, top);
+                            mma_terms<TE, TE, 2>(B_, x, b, top);
+                        }
+                        uint32_t b[TE][CT / 2][4];
+#pragma unroll
+                        for (int i = 0; i < TE; ++i)
+#pragma unroll
+                            for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kS + i * L::SB, 16 * ks, c0 / 8 + 2 * m));
+                        mma_terms<TI, TE, CT>(q_, y, b, top);
+                        mma_terms<TE, TE, CT>(k_, x, b, top);
+#pragma unroll
+                        for (int i = 0; i < TE; ++i)
+#pragma unroll
+                            for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kD + i * L::SB, 16 * ks, c0 / 8 + 2 * m));
+                        mma_terms<TE, TE, CT>(o_, e, b, top);
+                    }
+                }
+                if constexpr (F32) {
+                    add_to(A, tA);
+                    add_to(B, tB);
+                    add_to(aq, tq);
+                    add_to(ak, tk);
+                    add_to(ao, to);
+                }
+#pragma unroll
+                for (int i = tid; i < DW * NN / 8; i += GT) {       // <S, dS'>: both tiles have one layout
+                    float a[8], b[8];
+                    eight_at<TE>(a, base + L::kS + i * 16, L::SB);
+                    eight_at<TE>(b, base + L::kD + i * 16, L::SB);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) ss = fmaf(a[e], b[e], ss);
                 }
             }
-            if constexpr (F32) {
-                add_to(A, tA);
-                add_to(B, tB);
-                add_to(aq, tq);
-                add_to(ak, tk);
-                add_to(ao, to);
-            }
-#pragma unroll
-            for (int i = tid; i < DW * NN / 8; i += GT) {       // <S, dS'>: both tiles have one layout
-                float a[8], b[8];
-                eight_at<TE>(a, base + L::kS + i * 16, L::SB);
-                eight_at<TE>(b, base + L::kD + i * 16, L::SB);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(a[e], b[e], ss);
-            }
-        }
-        __syncthreads();                // the slice has been read, the scalars are there
-        // rows i = 16 wr + gr (+ 8), columns j = j0 + 8 m + 2 tc (+ 1)
-        float rows[2] = {}, tails[2] = {};
-        const bool near = sc->near != 0;
-        float rn[2], ro[2], rh[2], rl[2];           // rows: factors of n and o, the sums of log decays
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int i = 16 * wr + gr + 8 * e;
-            const float f = near ? sc->up[i] : 1.f;
-            rn[e] = f * sc->sq[i];
-            ro[e] = f * sc->rk[i];
-            rh[e] = sc->ghi[i];
-            rl[e] = sc->glo[i];
-        }
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            const int j = j0 + 8 * m + 2 * tc;
-            float cols[2] = {}, cf[2], ch[2], cl[2], bt[2];
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                cf[f] = (near ? sc->down[j + f] : 1.f) * sc->rk[j + f];
-                ch[f] = sc->ghi[j + f];
-                cl[f] = sc->glo[j + f];
-                bt[f] = sc->beta[j + f];
-            }
+            __syncthreads();                // the slice has been read, the scalars are there
+            // rows i = 16 wr + gr (+ 8), columns j = j0 + 8 m + 2 tc (+ 1)
+            float rows[2] = {}, tails[2] = {};
+            const bool near = sc->near != 0;
+            float rn[2], ro[2], rh[2], rl[2];           // rows: factors of n and o, the sums of log decays
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = 16 * wr + gr + 8 * e;
-                float vn[2], vo[2];
+                const float f = near ? sc->up[i] : 1.f;
+                rn[e] = f * sc->sq[i];
+                ro[e] = f * sc->rk[i];
+                rh[e] = sc->ghi[i];
+                rl[e] = sc->glo[i];
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int j = j0 + 8 * m + 2 * tc;
+                float cols[2] = {}, cf[2], ch[2], cl[2], bt[2];
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
-                    const float d = near ? cf[f] : cf[f] * fast_exp((rh[e] - ch[f]) + (rl[e] - cl[f]));
-                    const float nn = j + f <= i ? A[m][2 * e + f] * d * rn[e] : 0.f, oo = j + f < i ? B[m][2 * e + f] * d * ro[e] : 0.f;
-                    const float z = nn * QK[m][2 * e + f] - oo * KK[m][2 * e + f];
-                    if (j + f == i) {       // z_ii belongs to beta alone: g_i changes neither side of it
-                        sc->diag[i] = z;
-                    } else {
-                        cols[f] += z;
-                        rows[e] = fmaf(bt[f], z, rows[e]);
-                    }
-                    vn[f] = nn * bt[f];
-                    vo[f] = -oo * bt[f];
+                    cf[f] = (near ? sc->down[j + f] : 1.f) * sc->rk[j + f];
+                    ch[f] = sc->ghi[j + f];
+                    cl[f] = sc->glo[j + f];
+                    bt[f] = sc->beta[j + f];
                 }
-                uint32_t a[TE], b[TE];
-                split2<TE>(vn[0], vn[1], a);
-                split2<TE>(vo[0], vo[1], b);
-                const uint32_t to = base + tile<GC * 2>(i, j >> 3) + ((j & 7) << 1);
-#pragma unroll
-                for (int z = 0; z < TE; ++z) {
-                    st_b32(to + z * L::MB + L::kN, a[z]);
-                    st_b32(to + z * L::MB + L::kO, b[z]);
-                }
-            }
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                const float x = col_sum(cols[f]);
-                if (gr == 0) sc->col[wr][j + f] = x;
-            }
-        }
-        // what came through the states, over this warp's key channels
-        float fq[2], fk[2], fo[2], fb[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int i = 16 * wr + gr + 8 * e;
-            fq[e] = sc->qin[i];
-            fk[e] = sc->kin[i];
-            fo[e] = sc->kout[i];
-            fb[e] = sc->out[i];
-        }
-#pragma unroll
-        for (int t = 0; t < CT / 2; ++t) {
-            float2 qv[2][2], kv[2][2];
-            pairs_at<NB, TI>(qv, base + L::kQ, L::KB, 16 * wr, c0 / 16 + t);
-            pairs_at<NB, TI>(kv, base + L::kK, L::KB, 16 * wr, c0 / 16 + t);
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int m = 2 * t + u;
-                    const float q0 = fq[e] * aq[m][2 * e], q1 = fq[e] * aq[m][2 * e + 1];
-                    const float k0 = fk[e] * ak[m][2 * e], k1 = fk[e] * ak[m][2 * e + 1], o0 = ao[m][2 * e], o1 = ao[m][2 * e + 1];
-                    rows[e] += fmaf(qv[u][e].x, q0, qv[u][e].y * q1) - fmaf(kv[u][e].x, k0, kv[u][e].y * k1);
-                    tails[e] += fo[e] * fmaf(kv[u][e].x, o0, kv[u][e].y * o1);
-                    DQ[m][2 * e] += q0;
-                    DQ[m][2 * e + 1] += q1;
-                    DK[m][2 * e] += fmaf(fb[e], o0, -k0);
-                    DK[m][2 * e + 1] += fmaf(fb[e], o1, -k1);
-                }
-        }
+                    const int i = 16 * wr + gr + 8 * e;
+                    float vn[2], vo[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float x = quad_sum(rows[e]), y = quad_sum(tails[e]);
-            if (tc == 0) {
-                sc->row[wc][16 * wr + gr + 8 * e] = x;
-                sc->tail[wc][16 * wr + gr + 8 * e] = y;
-            }
-        }
+                    for (int f = 0; f < 2; ++f) {
+                        const float d = near ? cf[f] : cf[f] * fast_exp((rh[e] - ch[f]) + (rl[e] - cl[f]));
+                        const float nn = j + f <= i ? A[m][2 * e + f] * d * rn[e] : 0.f, oo = j + f < i ? B[m][2 * e + f] * d * ro[e] : 0.f;
+                        const float z = nn * QK[m][2 * e + f] - oo * KK[m][2 * e + f];
+                        if (j + f == i) {       // z_ii belongs to beta alone: g_i changes neither side of it
+                            sc->diag[i] = z;
+                        } else {
+                            cols[f] += z;
+                            rows[e] = fmaf(bt[f], z, rows[e]);
+                        }
+                        vn[f] = nn * bt[f];
+                        vo[f] = -oo * bt[f];
+                    }
+                    uint32_t a[TE], b[TE];
+                    split2<TE>(vn[0], vn[1], a);
+                    split2<TE>(vo[0], vo[1], b);
+                    const uint32_t to = base + tile<GC * 2>(i, j >> 3) + ((j & 7) << 1);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (lane == 0) sc->ss[warp] = ss;
-        __syncthreads();
-        float tQ[CT][4] = {}, tK[CT][4] = {};
-        float (&Q_)[CT][4] = F32 ? tQ : DQ, (&K_)[CT][4] = F32 ? tK : DK;
-#pragma unroll
-        for (int pass = 0; pass < (F32 ? 2 : 1); ++pass) {
-            const int top = F32 ? pass : -1;
-            // sq dQ += n K, rk dK -= o K: depth j up to this row block
-#pragma unroll 1
-            for (int kb = 0; kb <= wr; ++kb) {
-                uint32_t a[TE][4], d[TE][4], b[TI][CT / 2][4];
-#pragma unroll
-                for (int i = 0; i < TE; ++i) {
-                    ldsm4(a[i], addr_a<GC * 2>(base + L::kN + i * L::MB, 16 * wr, kb));
-                    ldsm4(d[i], addr_a<GC * 2>(base + L::kO + i * L::MB, 16 * wr, kb));
+                    for (int z = 0; z < TE; ++z) {
+                        st_b32(to + z * L::MB + L::kN, a[z]);
+                        st_b32(to + z * L::MB + L::kO, b[z]);
+                    }
                 }
 #pragma unroll
-                for (int i = 0; i < TI; ++i)
-#pragma unroll
-                    for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kK + i * L::KB, 16 * kb, c0 / 8 + 2 * m));
-                mma_terms<TE, TI, CT>(Q_, a, b, top);
-                mma_terms<TE, TI, CT>(K_, d, b, top);
-            }
-            // rk dK += n^T Q - o^T K: depth i from this row block on
-#pragma unroll 1
-            for (int ib = wr; ib < 4; ++ib) {
-                uint32_t a[TE][4], d[TE][4], b[TI][CT / 2][4];
-                const uint32_t at = tile<GC * 2>(16 * ib + (lane & 7) + ((lane >> 4) << 3), 2 * wr + ((lane >> 3) & 1));
-#pragma unroll
-                for (int i = 0; i < TE; ++i) {
-                    ldsm4t(a[i], base + L::kN + i * L::MB + at);
-                    ldsm4t(d[i], base + L::kO + i * L::MB + at);
+                for (int f = 0; f < 2; ++f) {
+                    const float x = col_sum(cols[f]);
+                    if (gr == 0) sc->col[wr][j + f] = x;
                 }
-#pragma unroll
-                for (int i = 0; i < TI; ++i)
-#pragma unroll
-                    for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kQ + i * L::KB, 16 * ib, c0 / 8 + 2 * m));
-                mma_terms<TE, TI, CT>(K_, a, b, top);
-#pragma unroll
-                for (int i = 0; i < TI; ++i)
-#pragma unroll
-                    for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(base + L::kK + i * L::KB, 16 * ib, c0 / 8 + 2 * m));
-                mma_terms<TE, TI, CT>(K_, d, b, top);
             }
-        }
-        if constexpr (F32) {
-            add_to(DQ, tQ);
-            add_to(DK, tK);
-        }
-        if (warp == 0) {                // dbeta and dg: two tokens per lane, sums in a fixed order
-            float db[2], dG[2], bt[2];
+            // what came through the states, over this warp's key channels
+            float fq[2], fk[2], fo[2], fb[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int i = 2 * lane + e;
-                const float t = (sc->tail[0][i] + sc->tail[1][i]) + (sc->tail[2][i] + sc->tail[3][i]);
-                const float c = (sc->col[0][i] + sc->col[1][i]) + (sc->col[2][i] + sc->col[3][i]);
-                db[e] = t + sc->diag[i] + c;
-                dG[e] = ((sc->row[0][i] + sc->row[1][i]) + (sc->row[2][i] + sc->row[3][i])) - sc->beta[i] * c;
-                bt[e] = sc->beta[i] * t;
+                const int i = 16 * wr + gr + 8 * e;
+                fq[e] = sc->qin[i];
+                fk[e] = sc->kin[i];
+                fo[e] = sc->kout[i];
+                fb[e] = sc->out[i];
             }
-            float x = lane < GT / 32 ? sc->ss[lane] : 0.f;
 #pragma unroll
-            for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-            // from a token on: what depends on G_i there; before it: what reaches the chunk's end from there
-            float later = dG[0] + dG[1], before = bt[0] + bt[1];
+            for (int t = 0; t < CT / 2; ++t) {
+                float2 qv[2][2], kv[2][2];
+                pairs_at<NB, TI>(qv, keys + L::kQ, L::KB, 16 * wr, c0 / 16 + t);
+                pairs_at<NB, TI>(kv, keys + L::kK, L::KB, 16 * wr, c0 / 16 + t);
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float z = __shfl_down_sync(0xffffffffu, later, o), w = __shfl_up_sync(0xffffffffu, before, o);
-                if (lane + o < 32) later += z;
-                if (lane >= o) before += w;
-            }
-            float up = __shfl_up_sync(0xffffffffu, before, 1), down = __shfl_down_sync(0xffffffffu, later, 1);
-            if (lane == 0) up = 0.f;
-            if (lane == 31) down = 0.f;
-            const float last = sc->whole * x;
-            const float dg[2] = {((dG[0] + dG[1]) + down) + (up + last), (dG[1] + down) + ((up + bt[0]) + last)};
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (2 * lane + e < n) {
-                    const long long at = (t0 + 2 * lane + e) * p.H + h;
-                    if constexpr (F32) {
-                        static_cast<float *>(p.dg)[at] = dg[e];
-                        static_cast<float *>(p.dbeta)[at] = db[e];
-                    } else {
-                        static_cast<__nv_bfloat16 *>(p.dg)[at] = __float2bfloat16(dg[e]);
-                        static_cast<__nv_bfloat16 *>(p.dbeta)[at] = __float2bfloat16(db[e]);
+                    for (int e = 0; e < 2; ++e) {
+                        const int m = 2 * t + u;
+                        const float q0 = fq[e] * aq[m][2 * e], q1 = fq[e] * aq[m][2 * e + 1];
+                        const float k0 = fk[e] * ak[m][2 * e], k1 = fk[e] * ak[m][2 * e + 1], o0 = ao[m][2 * e], o1 = ao[m][2 * e + 1];
+                        rows[e] += fmaf(qv[u][e].x, q0, qv[u][e].y * q1) - fmaf(kv[u][e].x, k0, kv[u][e].y * k1);
+                        tails[e] += fo[e] * fmaf(kv[u][e].x, o0, kv[u][e].y * o1);
+                        DQ[m][2 * e] += q0;
+                        DQ[m][2 * e + 1] += q1;
+                        DK[m][2 * e] += fmaf(fb[e], o0, -k0);
+                        DK[m][2 * e + 1] += fmaf(fb[e], o1, -k1);
                     }
-                }
-        }
-    }
-    // back through the lengths, and out
-    if (p.qk_norm) {
-        float dq[2] = {}, dk[2] = {};
-#pragma unroll
-        for (int t = 0; t < CT / 2; ++t) {
-            float2 qv[2][2], kv[2][2];
-            pairs_at<NB, TI>(qv, base + L::kQ, L::KB, 16 * wr, c0 / 16 + t);
-            pairs_at<NB, TI>(kv, base + L::kK, L::KB, 16 * wr, c0 / 16 + t);
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    dq[e] += fmaf(qv[u][e].x, DQ[2 * t + u][2 * e], qv[u][e].y * DQ[2 * t + u][2 * e + 1]);
-                    dk[e] += fmaf(kv[u][e].x, DK[2 * t + u][2 * e], kv[u][e].y * DK[2 * t + u][2 * e + 1]);
-                }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float x = quad_sum(dq[e]), y = quad_sum(dk[e]);
-            if (tc == 0) {
-                sc->dq[wc][16 * wr + gr + 8 * e] = x;
-                sc->dk[wc][16 * wr + gr + 8 * e] = y;
             }
-        }
-        __syncthreads();
-        float fq[2], fk[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int i = 16 * wr + gr + 8 * e;
-            const float rq = sc->sq[i] / p.scale, rk = sc->rk[i];
-            fq[e] = rq * rq * ((sc->dq[0][i] + sc->dq[1][i]) + (sc->dq[2][i] + sc->dq[3][i]));
-            fk[e] = rk * rk * ((sc->dk[0][i] + sc->dk[1][i]) + (sc->dk[2][i] + sc->dk[3][i]));
-        }
-#pragma unroll
-        for (int t = 0; t < CT / 2; ++t) {
-            float2 qv[2][2], kv[2][2];
-            pairs_at<NB, TI>(qv, base + L::kQ, L::KB, 16 * wr, c0 / 16 + t);
-            pairs_at<NB, TI>(kv, base + L::kK, L::KB, 16 * wr, c0 / 16 + t);
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int m = 2 * t + u;
-                    DQ[m][2 * e] = fmaf(-fq[e], qv[u][e].x, DQ[m][2 * e]);
-                    DQ[m][2 * e + 1] = fmaf(-fq[e], qv[u][e].y, DQ[m][2 * e + 1]);
-                    DK[m][2 * e] = fmaf(-fk[e], kv[u][e].x, DK[m][2 * e]);
-                    DK[m][2 * e + 1] = fmaf(-fk[e], kv[u][e].y, DK[m][2 * e + 1]);
+            for (int e = 0; e < 2; ++e) {
+                const float x = quad_sum(rows[e]), y = quad_sum(tails[e]);
+                if (tc == 0) {
+                    sc->row[wc][16 * wr + gr + 8 * e] = x;
+                    sc->tail[wc][16 * wr + gr + 8 * e] = y;
                 }
-        }
-    }
+            }
 #pragma unroll
-    for (int m = 0; m < CT; ++m)
+            for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (lane == 0) sc->ss[warp] = ss;
+            __syncthreads();
+            float tQ[CT][4] = {}, tK[CT][4] = {};
+            float (&Q_)[CT][4] = F32 ? tQ : DQ, (&K_)[CT][4] = F32 ? tK : DK;
 #pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-            const int i = 16 * wr + gr + 4 * e;
-            if (i >= n) continue;
-            const long long at = ((t0 + i) * p.Hk + hk) * NN + c0 + 8 * m + 2 * tc;
+            for (int pass = 0; pass < (F32 ? 2 : 1); ++pass) {
+                const int top = F32 ? pass : -1;
+                // sq dQ += n K, rk dK -= o K: depth j up to this row block
+#pragma unroll 1
+                for (int kb = 0; kb <= wr; ++kb) {
+                    uint32_t a[TE][4], d[TE][4], b[TI][CT / 2][4];
+#pragma unroll
+                    for (int i = 0; i < TE; ++i) {
+                        ldsm4(a[i], addr_a<GC * 2>(base + L::kN + i * L::MB, 16 * wr, kb));
+                        ldsm4(d[i], addr_a<GC * 2>(base + L::kO + i * L::MB, 16 * wr, kb));
+                    }
+#pragma unroll
+                    for (int i = 0; i < TI; ++i)
+#pragma unroll
+                        for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(keys + L::kK + i * L::KB, 16 * kb, c0 / 8 + 2 * m));
+                    mma_terms<TE, TI, CT>(Q_, a, b, top);
+                    mma_terms<TE, TI, CT>(K_, d, b, top);
+                }
+                // rk dK += n^T Q - o^T K: depth i from this row block on
+#pragma unroll 1
+                for (int ib = wr; ib < 4; ++ib) {
+                    uint32_t a[TE][4], d[TE][4], b[TI][CT / 2][4];
+                    const uint32_t at = tile<GC * 2>(16 * ib + (lane & 7) + ((lane >> 4) << 3), 2 * wr + ((lane >> 3) & 1));
+#pragma unroll
+                    for (int i = 0; i < TE; ++i) {
+                        ldsm4t(a[i], base + L::kN + i * L::MB + at);
+                        ldsm4t(d[i], base + L::kO + i * L::MB + at);
+                    }
+#pragma unroll
+                    for (int i = 0; i < TI; ++i)
+#pragma unroll
+                        for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(keys + L::kQ + i * L::KB, 16 * ib, c0 / 8 + 2 * m));
+                    mma_terms<TE, TI, CT>(K_, a, b, top);
+#pragma unroll
+                    for (int i = 0; i < TI; ++i)
+#pragma unroll
+                        for (int m = 0; m < CT / 2; ++m) ldsm4t(b[i][m], addr_bt<NB>(keys + L::kK + i * L::KB, 16 * ib, c0 / 8 + 2 * m));
+                    mma_terms<TE, TI, CT>(K_, d, b, top);
+                }
+            }
             if constexpr (F32) {
-                *reinterpret_cast<float2 *>(static_cast<float *>(p.dq) + at) = make_float2(DQ[m][e], DQ[m][e + 1]);
-                *reinterpret_cast<float2 *>(static_cast<float *>(p.dk) + at) = make_float2(DK[m][e], DK[m][e + 1]);
-            } else {
-                *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.dq) + at) = pack(DQ[m][e], DQ[m][e + 1]);
-                *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.dk) + at) = pack(DK[m][e], DK[m][e + 1]);
+                add_to(DQ, tQ);
+                add_to(DK, tK);
+            }
+            if (warp == scalar_warp) {                // dbeta and dg: two tokens per lane, sums in a fixed order
+                float db[2], dG[2], bt[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int i = 2 * lane + e;
+                    const float t = (sc->tail[0][i] + sc->tail[1][i]) + (sc->tail[2][i] + sc->tail[3][i]);
+                    const float c = (sc->col[0][i] + sc->col[1][i]) + (sc->col[2][i] + sc->col[3][i]);
+                    db[e] = t + sc->diag[i] + c;
+                    dG[e] = ((sc->row[0][i] + sc->row[1][i]) + (sc->row[2][i] + sc->row[3][i])) - sc->beta[i] * c;
+                    bt[e] = sc->beta[i] * t;
+                }
+                float x = lane < GT / 32 ? sc->ss[lane] : 0.f;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                // from a token on: what depends on G_i there; before it: what reaches the chunk's end from there
+                float later = dG[0] + dG[1], before = bt[0] + bt[1];
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float z = __shfl_down_sync(0xffffffffu, later, o), w = __shfl_up_sync(0xffffffffu, before, o);
+                    if (lane + o < 32) later += z;
+                    if (lane >= o) before += w;
+                }
+                float up = __shfl_up_sync(0xffffffffu, before, 1), down = __shfl_down_sync(0xffffffffu, later, 1);
+                if (lane == 0) up = 0.f;
+                if (lane == 31) down = 0.f;
+                const float last = sc->whole * x;
+                const float dg[2] = {((dG[0] + dG[1]) + down) + (up + last), (dG[1] + down) + ((up + bt[0]) + last)};
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (2 * lane + e < n) {
+                        const long long at = (t0 + 2 * lane + e) * p.H + h;
+                        if constexpr (F32) {
+                            static_cast<float *>(p.dg)[at] = dg[e];
+                            static_cast<float *>(p.dbeta)[at] = db[e];
+                        } else {
+                            static_cast<__nv_bfloat16 *>(p.dg)[at] = __float2bfloat16(dg[e]);
+                            static_cast<__nv_bfloat16 *>(p.dbeta)[at] = __float2bfloat16(db[e]);
+                        }
+                    }
+            }
+            if constexpr (L::AHEAD) base = both - base;
+        }
+        // back through the lengths, and out
+        if (p.qk_norm) {
+            float dq[2] = {}, dk[2] = {};
+#pragma unroll
+            for (int t = 0; t < CT / 2; ++t) {
+                float2 qv[2][2], kv[2][2];
+                pairs_at<NB, TI>(qv, keys + L::kQ, L::KB, 16 * wr, c0 / 16 + t);
+                pairs_at<NB, TI>(kv, keys + L::kK, L::KB, 16 * wr, c0 / 16 + t);
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        dq[e] += fmaf(qv[u][e].x, DQ[2 * t + u][2 * e], qv[u][e].y * DQ[2 * t + u][2 * e + 1]);
+                        dk[e] += fmaf(kv[u][e].x, DK[2 * t + u][2 * e], kv[u][e].y * DK[2 * t + u][2 * e + 1]);
+                    }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float x = quad_sum(dq[e]), y = quad_sum(dk[e]);
+                if (tc == 0) {
+                    sc->dq[wc][16 * wr + gr + 8 * e] = x;
+                    sc->dk[wc][16 * wr + gr + 8 * e] = y;
+                }
+            }
+            __syncthreads();
+            float fq[2], fk[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 16 * wr + gr + 8 * e;
+                const float rq = sc->sq[i] / p.scale, rk = sc->rk[i];
+                fq[e] = rq * rq * ((sc->dq[0][i] + sc->dq[1][i]) + (sc->dq[2][i] + sc->dq[3][i]));
+                fk[e] = rk * rk * ((sc->dk[0][i] + sc->dk[1][i]) + (sc->dk[2][i] + sc->dk[3][i]));
+            }
+#pragma unroll
+            for (int t = 0; t < CT / 2; ++t) {
+                float2 qv[2][2], kv[2][2];
+                pairs_at<NB, TI>(qv, keys + L::kQ, L::KB, 16 * wr, c0 / 16 + t);
+                pairs_at<NB, TI>(kv, keys + L::kK, L::KB, 16 * wr, c0 / 16 + t);
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int m = 2 * t + u;
+                        DQ[m][2 * e] = fmaf(-fq[e], qv[u][e].x, DQ[m][2 * e]);
+                        DQ[m][2 * e + 1] = fmaf(-fq[e], qv[u][e].y, DQ[m][2 * e + 1]);
+                        DK[m][2 * e] = fmaf(-fk[e], kv[u][e].x, DK[m][2 * e]);
+                        DK[m][2 * e + 1] = fmaf(-fk[e], kv[u][e].y, DK[m][2 * e + 1]);
+                    }
             }
         }
+#pragma unroll
+        for (int m = 0; m < CT; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const int i = 16 * wr + gr + 4 * e;
+                if (i >= n) continue;
+                const long long at = ((t0 + i) * p.Hk + hk) * NN + c0 + 8 * m + 2 * tc;
+                if constexpr (F32) {
+                    *reinterpret_cast<float2 *>(static_cast<float *>(p.dq) + at) = make_float2(DQ[m][e], DQ[m][e + 1]);
+                    *reinterpret_cast<float2 *>(static_cast<float *>(p.dk) + at) = make_float2(DK[m][e], DK[m][e + 1]);
+                } else {
+                    *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.dq) + at) = pack(DQ[m][e], DQ[m][e + 1]);
+                    *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.dk) + at) = pack(DK[m][e], DK[m][e + 1]);
+                }
+            }
+        if constexpr (!L::AHEAD) return;
+        cur = sc->next;
+        if (cur.n == 0) return;
+        keys = both - keys;
+    }
 }
 
 }  // namespace
@@ -916,12 +978,12 @@ template <int NN, int RW, bool F32, int GROUPS>
 cudaError_t launch_t(const DeltaArgs &p, long long slots) {
     constexpr int fwd_bytes = Layout<NN, RW, F32, true, GROUPS>::total, rev_bytes = RevLayout<NN, RW, F32, GROUPS>::total;
     constexpr int sweep_bytes = fwd_bytes > rev_bytes ? fwd_bytes : rev_bytes;
-    constexpr int grad_bytes = GradLayout<NN, F32>::kF + int(sizeof(GradScalars));
+    using G = GradLayout<NN, F32>;
     const void *sweeps = reinterpret_cast<const void *>(delta_sweeps_kernel<NN, RW, F32, GROUPS>);
     const void *grad = reinterpret_cast<const void *>(delta_grad_kernel<NN, F32>);
     cudaError_t e = allow_dynamic_smem(sweeps, sweep_bytes);
     if (e != cudaSuccess) return e;
-    e = allow_dynamic_smem(grad, grad_bytes);
+    e = allow_dynamic_smem(grad, G::total);
     if (e != cudaSuccess) return e;
     // Together where that fills SMs that one sweep leaves idle (and at N = 128, where a CTA has an SM to itself:
     // 541 us against 584 for seven packed sequences of 8 heads); in turn otherwise, since blocks of the two kinds
@@ -933,7 +995,8 @@ cudaError_t launch_t(const DeltaArgs &p, long long slots) {
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    delta_grad_kernel<NN, F32><<<unsigned(slots) * p.Hk, GT, grad_bytes, p.stream>>>(p);
+    const long long tasks = slots * p.Hk;
+    delta_grad_kernel<NN, F32><<<unsigned(G::AHEAD ? std::min(tasks, 148ll) : tasks), GT, G::total, p.stream>>>(p, unsigned(tasks));
     return cudaGetLastError();
 }
 
