@@ -2,11 +2,12 @@
 // vocabulary, and the reordering of the states' rows.
 //
 // Selection reads the logits once. beam_part_kernel: a CTA takes a segment of one row into registers (packed, as
-// loaded), sums its exponentials against its own maximum, and finds its M best elements. The M-th
-// largest of the 256 threads' own maxima is a floor for the M-th best element: M elements at least reach
-// it, and those above it lie in fewer than M threads. What reaches the floor is gathered and placed by
-// counting; only where more elements equal the floor than there is room for are they taken in the
-// order of their index instead. The lists hold 64-bit keys, order-preserving bits of the value above the
+// loaded), sums its exponentials against its own maximum, and finds its M best elements. Each of the 8 warps finds
+// the M/8-th largest of its threads' own maxima; the least of these is a floor for the M-th best element, and what
+// reaches it (on logits without order about 5 M/2 elements) is gathered and placed by counting. Where the
+// elements lie so that more than 2 M + 64 reach it, the M-th largest of all threads' maxima is the floor: what is
+// above that lies in fewer than M threads. Only where more elements equal that floor than there is room for are they
+// taken in the order of their index instead. The lists hold 64-bit keys, order-preserving bits of the value above the
 // complement of the index, so that keys never tie and equal values go to the lowest index.
 // beam_pick_kernel: one CTA per request joins the segments' sums in fp64, merges the sorted lists of a row and
 // then those of the rows. An element's place in a merged list is its place in its own plus, for every
@@ -14,6 +15,8 @@
 #include "beam.cuh"
 
 #include <cuda_bf16.h>
+
+#include <limits.h>
 
 #include <algorithm>
 
@@ -116,28 +119,42 @@ __device__ __forceinline__ float largest(const uint4 (&v)[NV], const __nv_bfloat
     for (int j = 0; j < NV; ++j) m = __hmax2(__hmax2(__hmax2(m, b2(v[j].x)), b2(v[j].y)), __hmax2(b2(v[j].z), b2(v[j].w)));
     return fmaxf(__low2float(m), __high2float(m));
 }
-// Calls f(value, place in the vector) for the elements of a vector that are at least `least`.
-template <class F>
-__device__ __forceinline__ void for_at_least(const uint4 &v, float least, const float *, F f) {
-    float x[4];
-    unpack(v, x);
+// Which elements are at least `least`, a bit each: bf16 word 4 j + i of the first four vectors in bits 4 j + i (its first
+// element) and 16 more (its second) of the first mask, of the others in the second; fp32 element 4 j + e in bit
+// 4 j + e of the first. place(mask, bit): element of its vector + 8 or 4 times the vector's number.
+template <int NV>
+__device__ __forceinline__ void at_least(const uint4 (&v)[NV], float least, uint32_t (&mask)[2], const float *) {
+    mask[0] = mask[1] = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (x[e] >= least) f(x[e], e);
-}
-template <class F>
-__device__ __forceinline__ void for_at_least(const uint4 &v, float least, const __nv_bfloat16 *, F f) {
-    const __nv_bfloat162 l = __float2bfloat162_rn(least);      // a logit: exact
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int j = 0; j < NV; ++j) {
+        float x[4];
+        unpack(v[j], x);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t hit = __hge2_mask(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]), l);
-        if (hit) {
-            if (hit & 0xffffu) f(__uint_as_float(w[i] << 16), 2 * i);
-            if (hit >> 16) f(__uint_as_float(w[i] & 0xffff0000u), 2 * i + 1);
-        }
+        for (int e = 0; e < 4; ++e) mask[0] |= x[e] >= least ? 1u << (4 * j + e) : 0u;
     }
 }
+template <int NV>
+__device__ __forceinline__ void at_least(const uint4 (&v)[NV], float least, uint32_t (&mask)[2], const __nv_bfloat16 *) {
+    const __nv_bfloat162 l = __float2bfloat162_rn(least);      // a logit: exact
+    mask[0] = mask[1] = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            mask[j >> 2] |= __hge2_mask(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]), l) & (0x00010001u << (4 * (j & 3) + i));
+    }
+}
+__device__ __forceinline__ int place(int, int bit, const float *) { return bit; }
+__device__ __forceinline__ int place(int mask, int bit, const __nv_bfloat16 *) { return 32 * mask + 2 * (bit & 15) + (bit >> 4); }
+
+__device__ __forceinline__ float value(const float *p) { return __ldg(p); }
+__device__ __forceinline__ float value(const __nv_bfloat16 *p) {
+    return __uint_as_float(uint32_t(__ldg(reinterpret_cast<const unsigned short *>(p))) << 16);
+}
+// The least value that is above -inf.
+__device__ __forceinline__ float lowest(const float *) { return __uint_as_float(0xff7fffffu); }
+__device__ __forceinline__ float lowest(const __nv_bfloat16 *) { return __uint_as_float(0xff7f0000u); }
 
 // Sorts one value per lane over the warp, largest in lane 0.
 __device__ __forceinline__ uint32_t warp_sort_desc(uint32_t k) {
@@ -159,6 +176,32 @@ __device__ __forceinline__ float quick_exp(float x) {
     return y;
 }
 
+// The same of x + c and y + c, and a sum of pairs: two numbers to an instruction.
+__device__ __forceinline__ unsigned long long pair(float x, float y) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 halves(unsigned long long r) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+    return v;
+}
+__device__ __forceinline__ float2 quick_exp2(float x, float y, float c) {
+    unsigned long long r;
+    asm("{\n\t.reg .b64 t;\n\tadd.rn.f32x2 t, %1, %2;\n\tmul.rn.f32x2 %0, t, %3;\n\t}"
+        : "=l"(r) : "l"(pair(x, y)), "l"(pair(c, c)), "l"(pair(1.4426950408889634f, 1.4426950408889634f)));
+    float2 v = halves(r);
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(v.x));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(v.y));
+    return v;
+}
+__device__ __forceinline__ void add2(float2 &a, float2 b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a.x, a.y)), "l"(pair(b.x, b.y)));
+    a = halves(r);
+}
+
 // How many of the n keys, sorted from the largest down, are above x.
 template <class U>
 __device__ __forceinline__ int count_above(const U *list, int n, U x) {
@@ -171,11 +214,18 @@ __device__ __forceinline__ int count_above(const U *list, int n, U x) {
     return lo;
 }
 
+// What beam_part_kernel ranks without a second look, and what it has room for in all.
+__host__ __device__ __forceinline__ int few_of(int M) { return 2 * M + 64; }
+__host__ __device__ __forceinline__ int room_of(int M, int elements) {
+    const int all = M * (elements + 1), few = few_of(M);
+    return all > few ? all : few;
+}
+
 template <class Tin, int NV>
-__global__ void __launch_bounds__(kT, 6) beam_part_kernel(const BeamArgs p, int splits) {
+__global__ void __launch_bounds__(kT, NV > 4 ? 5 : 6) beam_part_kernel(const BeamArgs p, int splits) {
     constexpr int VW = 16 / sizeof(Tin), EPT = NV * VW, SEG = kT * EPT, W = kT / 32;
-    extern __shared__ unsigned long long cand[];          // [M * EPT + M]
-    __shared__ uint32_t s_sort[W][32], s_floor;
+    extern __shared__ unsigned long long cand[];          // [room_of(M, EPT)]
+    __shared__ uint32_t s_sort[W][32], s_floor, s_top[W], s_low[W];
     __shared__ double s_sum[W];
     __shared__ int s_n, s_ties[W];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");     // the picking kernel may take its place
@@ -198,21 +248,31 @@ __global__ void __launch_bounds__(kT, 6) beam_part_kernel(const BeamArgs p, int 
         s_n = 0;
     }
     const float top = largest<NV>(v, static_cast<const Tin *>(nullptr));
-    uint32_t sorted = warp_sort_desc(order_bits(top == 0.f ? 0.f : top));
-    s_sort[warp][lane] = sorted;
+    const uint32_t own_top = order_bits(top == 0.f ? 0.f : top);
+    // the warp's largest, and the last of as many as it has to hold for W warps to hold M
+    uint32_t first = 0, last = 0, left = own_top;
+    for (int i = 0; i < (p.M + W - 1) / W; ++i) {
+        last = __reduce_max_sync(0xffffffffu, left);
+        if (i == 0) first = last;
+        if (__ffs(__ballot_sync(0xffffffffu, left == last)) - 1 == lane) left = 0;
+    }
+    if (lane == 0) {
+        s_top[warp] = first;
+        s_low[warp] = last;
+    }
     __syncthreads();
-    uint32_t peak = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) peak = max(peak, s_sort[w][0]);
+    const uint32_t peak = __reduce_max_sync(0xffffffffu, s_top[lane % W]);
+    uint32_t low = __reduce_min_sync(0xffffffffu, s_low[lane % W]);
     const float ctop = peak ? order_value(peak) : -INFINITY, ref = peak ? ctop : 0.f;
-    float sum = 0.f;
+    float2 sums = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         float x[VW];
         unpack(v[j], x);
 #pragma unroll
-        for (int e = 0; e < VW; ++e) sum += quick_exp(x[e] - ref);
+        for (int e = 0; e < VW; e += 2) add2(sums, quick_exp2(x[e], x[e + 1], -ref));
     }
+    float sum = sums.x + sums.y;
     if (sum != sum) {                                      // a NaN among them counts as -inf
         sum = 0.f;
 #pragma unroll
@@ -227,70 +287,86 @@ __global__ void __launch_bounds__(kT, 6) beam_part_kernel(const BeamArgs p, int 
 #pragma unroll
     for (int o = 16; o; o >>= 1) ds += __shfl_xor_sync(0xffffffffu, ds, o);
     if (lane == 0) s_sum[warp] = ds;
-    // the M-th largest of the threads' maxima (0: fewer than M threads hold anything): up to 32, by merging the
-    // sorted warps pairwise; above, by counting in the other warps' lists
-    if (p.M <= 32) {
-#pragma unroll
-        for (int step = 1; step < W; step *= 2) {
-            __syncthreads();
-            if (warp % (2 * step) == 0) {
-                sorted = max(sorted, s_sort[warp + step][31 - lane]);      // the 32 largest of both, rising then falling
-#pragma unroll
-                for (int stride = 16; stride; stride >>= 1) {
-                    const uint32_t o = __shfl_xor_sync(0xffffffffu, sorted, stride);
-                    sorted = (lane & stride) == 0 ? max(sorted, o) : min(sorted, o);
-                }
-                s_sort[warp][lane] = sorted;
+    constexpr const Tin *type = nullptr;
+    float least = low ? order_value(low) : lowest(type);
+    // Calls f(value, index) for this thread's elements that reach the floor. They are few: their values are read again, so
+    // that there is one copy of what is done with them and not one per element.
+    auto each = [&](auto f) {
+        if (!(top >= least)) return;
+        uint32_t mask[2];
+        at_least<NV>(v, least, mask, type);
+#pragma unroll 1
+        for (int m = 0; m < (NV * VW > 32 ? 2 : 1); ++m)
+            for (uint32_t left = m ? mask[1] : mask[0]; left; left &= left - 1) {
+                const int e = place(m, __ffs(left) - 1, type), i = at + e / VW * (kT * VW) + e % VW;
+                f(value(base + i), i);
             }
-        }
-        if (warp == 0 && lane == p.M - 1) s_floor = sorted;
-    } else if (sorted) {
-        int above = lane, same = 0;                        // equal values: those of lower warps come first
-        for (int w = 0; w < W; ++w)
-            if (w != warp) {
-                const int a = count_above(s_sort[w], 32, sorted);
-                above += a;
-                if (w < warp) same += count_above(s_sort[w], 32, sorted - 1) - a;
-            }
-        if (above + same == p.M - 1) s_floor = sorted;
-    }
-    __syncthreads();
-    const uint32_t low = s_floor;
-    const float least = low ? order_value(low) : -INFINITY;
-    const int room = p.M * EPT;
-    if (top >= least) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            for_at_least(v[j], least, static_cast<const Tin *>(nullptr), [&](float x, int e) {
-                const unsigned long long key = make_key(x, uint32_t(at + j * kT * VW + e));
-                if (key) {
-                    const int to = atomicAdd(&s_n, 1);
-                    if (to < room) cand[to] = key;
-                }
-            });
-    }
-    __syncthreads();
+    };
+    auto gather = [&](int most) {
+        each([&](float x, int i) {
+            const int to = atomicAdd(&s_n, 1);
+            if (to < most) cand[to] = make_key(x, uint32_t(i));
+        });
+        __syncthreads();
+    };
+    const int few = few_of(p.M), room = max(few, p.M * EPT);
+    gather(few);
     int n = s_n;
-    if (n > room) {             // more elements equal the floor than there is room for: the lowest indices of them
+    if (n > few) {              // the same with the best floor that the threads' maxima give
+        __syncthreads();
+        if (tid == 0) s_n = 0;
+        // the M-th largest of the threads' maxima (0: fewer than M threads hold anything): up to 32, by merging the
+        // sorted warps pairwise; above, by counting in the other warps' lists
+        uint32_t sorted = warp_sort_desc(own_top);
+        s_sort[warp][lane] = sorted;
+        __syncthreads();
+        if (p.M <= 32) {
+#pragma unroll
+            for (int step = 1; step < W; step *= 2) {
+                __syncthreads();
+                if (warp % (2 * step) == 0) {
+                    sorted = max(sorted, s_sort[warp + step][31 - lane]);      // the 32 largest of both, rising then falling
+#pragma unroll
+                    for (int stride = 16; stride; stride >>= 1) {
+                        const uint32_t o = __shfl_xor_sync(0xffffffffu, sorted, stride);
+                        sorted = (lane & stride) == 0 ? max(sorted, o) : min(sorted, o);
+                    }
+                    s_sort[warp][lane] = sorted;
+                }
+            }
+            if (warp == 0 && lane == p.M - 1) s_floor = sorted;
+        } else if (sorted) {
+            int above = lane, same = 0;                        // equal values: those of lower warps come first
+            for (int w = 0; w < W; ++w)
+                if (w != warp) {
+                    const int a = count_above(s_sort[w], 32, sorted);
+                    above += a;
+                    if (w < warp) same += count_above(s_sort[w], 32, sorted - 1) - a;
+                }
+            if (above + same == p.M - 1) s_floor = sorted;
+        }
+        __syncthreads();
+        low = s_floor;
+        least = low ? order_value(low) : lowest(type);
+        gather(room);
+        n = s_n;
+    }
+    if (n > room) {             // more elements equal that floor than there is room for: the lowest indices of them
         __syncthreads();
         if (tid == 0) s_n = 0;
         __syncthreads();
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            for_at_least(v[j], least, static_cast<const Tin *>(nullptr), [&](float x, int e) {
-                if (x > least) cand[atomicAdd(&s_n, 1)] = make_key(x, uint32_t(at + j * kT * VW + e));
-            });
+        each([&](float x, int i) {
+            if (x > least) cand[atomicAdd(&s_n, 1)] = make_key(x, uint32_t(i));
+        });
         __syncthreads();
         n = s_n;                                           // in fewer than M threads
         const int need = p.M - min(n, p.M);
         int got = 0;
 #pragma unroll 1
         for (int j = 0; j < NV && got < need; ++j) {
-            uint4 u = v[0];
-#pragma unroll
-            for (int i = 1; i < NV; ++i) u = i == j ? v[i] : u;
+            const int i0 = at + j * kT * VW, ends = min(VW, p.V - i0);
             int mine = 0;
-            for_at_least(u, least, static_cast<const Tin *>(nullptr), [&](float x, int) { mine += x == least; });
+            for (int e = 0; e < ends; ++e) mine += value(base + i0 + e) == least;
             int before = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -305,12 +381,11 @@ __global__ void __launch_bounds__(kT, 6) beam_part_kernel(const BeamArgs p, int 
                 all += s_ties[w];
             }
             int to = got + before - mine;
-            for_at_least(u, least, static_cast<const Tin *>(nullptr), [&](float x, int e) {
-                if (x == least) {
-                    if (to < need) cand[n + to] = make_key(x, uint32_t(at + j * kT * VW + e));
+            for (int e = 0; e < ends; ++e)
+                if (value(base + i0 + e) == least) {
+                    if (to < need) cand[n + to] = make_key(least, uint32_t(i0 + e));
                     ++to;
                 }
-            });
             got += all;
             __syncthreads();
         }
@@ -319,11 +394,13 @@ __global__ void __launch_bounds__(kT, 6) beam_part_kernel(const BeamArgs p, int 
     Part *part = static_cast<Part *>(p.ws);
     unsigned long long *list = reinterpret_cast<unsigned long long *>(part + size_t(p.B) * p.K * splits) +
                                size_t(blockIdx.x) * p.M;
-    for (int i = tid; i < n; i += kT) {
-        const unsigned long long c = cand[i];
+    for (int i = tid >> 2; i < ((n + 7) & ~7); i += kT / 4) {       // four threads to a candidate, whole warps
+        const unsigned long long c = i < n ? cand[i] : 0;
         int rank = 0;
-        for (int j = 0; j < n; ++j) rank += cand[j] > c;
-        if (rank < p.M) list[rank] = c;
+        for (int j = tid & 3; j < n; j += 4) rank += cand[j] > c;
+        rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+        rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+        if (i < n && (tid & 3) == 0 && rank < p.M) list[rank] = c;
     }
     for (int i = n + tid; i < p.M; i += kT) list[i] = 0;
     if (tid == 0) {
@@ -484,22 +561,41 @@ cudaError_t reorder_t(int L, int B, int K, size_t row_bytes, const int *parents,
 
 // ---- host side ---------------------------------------------------------------------------------------
 
-// Elements per thread of beam_part_kernel: four vectors of 16 bytes (32 bf16, 16 fp32), or 8 elements where
-// that would leave SMs without a segment.
-int elements_per_thread(int B, int K, int V, int whole) {
-    return (long long)B * K * ((V - 1) / (kT * whole) + 1) < 2 * 148 ? 8 : whole;
+// Vectors of 16 bytes per thread of beam_part_kernel. A segment costs about as much as three vectors on top of its
+// own, so that four to six are taken by where the segments end: a row of 50277 bf16 makes five segments of five
+// instead of six and a seventh of four. One or two (8 elements) where more would leave SMs without a segment.
+int vectors_of(int B, int K, int V, int vw) {
+    int best = 4;
+    long long least = LLONG_MAX;
+    for (int n = 4; n <= 6; ++n) {
+        const long long cost = ((V - 1) / (kT * vw * n) + 1) * (n + 3ll);
+        if (cost < least) {
+            least = cost;
+            best = n;
+        }
+    }
+    return (long long)B * K * ((V - 1) / (kT * vw * best) + 1) < 2 * 148 ? 8 / vw : best;
 }
-int segments(int B, int K, int V, int whole) { return (V - 1) / (kT * elements_per_thread(B, K, V, whole)) + 1; }
-int whole_of(wkv7_dtype dt) { return dt == WKV7_BF16 ? 32 : 16; }
+int segments(int B, int K, int V, int vw) { return (V - 1) / (kT * vw * vectors_of(B, K, V, vw)) + 1; }
+int width_of(wkv7_dtype dt) { return dt == WKV7_BF16 ? 8 : 4; }
 
+template <class Tin, int NV>
+cudaError_t part_t(const BeamArgs &p, int splits) {
+    const unsigned grid = unsigned(p.B) * unsigned(p.K) * unsigned(splits);
+    const size_t smem = size_t(room_of(p.M, NV * (16 / int(sizeof(Tin))))) * 8;         // at most 25 KB
+    beam_part_kernel<Tin, NV><<<grid, kT, smem, p.stream>>>(p, splits);
+    return cudaGetLastError();
+}
 template <class Tin>
 cudaError_t select_t(const BeamArgs &p) {
-    const int whole = whole_of(p.dt), splits = segments(p.B, p.K, p.V, whole), ept = elements_per_thread(p.B, p.K, p.V, whole);
-    const unsigned grid = unsigned(p.B) * unsigned(p.K) * unsigned(splits);
-    const size_t smem = size_t(p.M) * (ept + 1) * 8;      // at most 16.5 KB
-    if (ept == 8) beam_part_kernel<Tin, sizeof(Tin) / 2><<<grid, kT, smem, p.stream>>>(p, splits);
-    else beam_part_kernel<Tin, 4><<<grid, kT, smem, p.stream>>>(p, splits);
-    return cudaGetLastError();
+    constexpr int vw = 16 / int(sizeof(Tin));
+    const int splits = segments(p.B, p.K, p.V, vw);
+    switch (vectors_of(p.B, p.K, p.V, vw)) {
+        case 4: return part_t<Tin, 4>(p, splits);
+        case 5: return part_t<Tin, 5>(p, splits);
+        case 6: return part_t<Tin, 6>(p, splits);
+        default: return part_t<Tin, 8 / vw>(p, splits);
+    }
 }
 
 }  // namespace
@@ -507,13 +603,13 @@ cudaError_t select_t(const BeamArgs &p) {
 cudaError_t allow_dynamic_smem(const void *kernel, int bytes);
 
 size_t beam_select_workspace(int B, int K, int V, int M) {
-    const int n = std::max(segments(B, K, V, 16), segments(B, K, V, 32));     // either type's
+    const int n = std::max(segments(B, K, V, 4), segments(B, K, V, 8));       // either type's
     return size_t(B) * K * size_t(n) * (sizeof(Part) + size_t(M) * 8);
 }
 
 cudaError_t launch_beam_select(const BeamArgs &p) {
     constexpr int most = 160 * 1024;
-    const int splits = segments(p.B, p.K, p.V, whole_of(p.dt));
+    const int splits = segments(p.B, p.K, p.V, width_of(p.dt));
     const size_t rows = size_t(p.K) * p.M * 16, lists = size_t(p.K) * splits * p.M * 8;     // rows: at most 64 KB
     const bool staged = rows + lists <= most;
     cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(beam_pick_kernel), most);
