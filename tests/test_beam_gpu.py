@@ -43,6 +43,21 @@ def test_select(cuda_device, B, K, V, M, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("B,K,V,M", [(1, 64, 50277, 64), (1, 2, 600_011, 33), (3, 33, 20_000, 7)])
+def test_select_many_lists(cuda_device, B, K, V, M, dt):
+    """More lists than fit shared memory, more than a warp has lanes for, more rows than lanes."""
+    check(cuda_device, *draw(B, K, V, dt, B + V), M)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_select_ties_between_rows_go_to_the_lowest_beam(cuda_device, dt):
+    """64 equal rows with equal scores: every place is a tie between all beams."""
+    x, _ = draw(1, 1, 3001, dt, 9)
+    check(cuda_device, x.expand(1, 64, 3001).contiguous(), torch.zeros(1, 64), 64)
+    check(cuda_device, x.expand(1, 40, 3001).contiguous(), (torch.arange(40) % 3 - 1).float()[None], 50)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_select_ties_go_to_the_lowest_index(cuda_device, dt):
     """Equal logits everywhere, and a few distinct values in coarse steps."""
     x, s = draw(2, 3, 20011, dt, 5)
