@@ -35,8 +35,10 @@ struct RevLayout {
     static constexpr int KB = TI * C * NN * 2, YB = TI * C * RW * 32;
     static constexpr int kK = 0, kQ = KB, kY = 2 * KB, kW = kY + YB, kP = kW + 3 * kTri, kS = kP + TP * kTri;
     static constexpr int stage = (kS + int(sizeof(Scalars)) + 255) / 256 * 256;
-    static constexpr int stages = F32 ? (NN == 64 ? 4 : 3) : (NN == 64 && GROUPS == 2 ? 5 : 6);
-    static constexpr int total = stages * stage + GROUPS * int(sizeof(PrepScratch));
+    static constexpr int stages = F32 ? (NN == 64 ? 4 : 3) : (GROUPS == 2 ? 4 : 6);
+    static constexpr int own = F32 ? 0 : 64 * NN;
+    static constexpr int kOwn = stages * stage, kPrep = kOwn + RW * own;
+    static constexpr int total = kPrep + GROUPS * int(sizeof(PrepScratch));
     static constexpr int meet = RW * 32 + kGroup;
 };
 
@@ -60,7 +62,7 @@ __device__ __forceinline__ void reverse_sweep(const DeltaArgs &p, unsigned block
     // step r takes chunk chunks - 1 - r
     if (warp >= RW) {
         const int group = (warp - RW) >> 1, tid = (threadIdx.x - RW * 32) % kGroup;
-        PrepScratch *ps = reinterpret_cast<PrepScratch *>(sm + L::stages * L::stage) + group;
+        PrepScratch *ps = reinterpret_cast<PrepScratch *>(sm + L::kPrep) + group;
         const long long first = t0 + (long long)(chunks - 1 - group) * C;
         RowLoader<NN, F32> k(p.k, first, (long long)hk * NN, p.ks, tid), q(p.q, first, (long long)hk * NN, p.qs, tid);
         RowLoader<RW * 16, F32> dy(p.dy, first, (long long)h * NN + row0, (long long)p.H * NN, tid);
@@ -122,7 +124,7 @@ __device__ __forceinline__ void reverse_sweep(const DeltaArgs &p, unsigned block
         const Scalars *sc = reinterpret_cast<const Scalars *>(sm + (r % L::stages) * L::stage + L::kS);
         const long long t = t0 + (long long)c * C;
         const int n_tok = int(min((long long)C, t1 - t));
-        if (r == 0 || c % 2 == 1) keep_state<F32, NN>(p.keep_dS, p.keep_second, (slot0 + c / 2) * p.H + h, row, S);
+        if (r == 0 || c % 2 == 1) keep_state<F32, NN>(p.keep_dS, p.keep_second, (slot0 + c / 2) * p.H + h, row, S, base + L::kOwn + warp * L::own);
         bar_sync(full + r % L::stages, L::meet);
         // dE^T = out (dS K^T) + dY^T P
         Acc<F32, 4> ea, xa;
@@ -267,35 +269,8 @@ __device__ __forceinline__ void reverse_sweep(const DeltaArgs &p, unsigned block
                     const int i = 8 * n + 2 * tc + (e & 1);
                     if (i < n_tok) dv[(t + i) * ys + gr + 8 * (e >> 1)] = X[n][e];
                 }
-        } else {                    // through dY's place (this warp's own columns), in two terms
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                __syncwarp();
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    uint32_t o[4];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float *x = &X[2 * m + i][2 * e];
-                            o[2 * i + e] = pack(x[0], x[1]);
-                            x[0] -= lo_f(o[2 * i + e]);
-                            x[1] -= hi_f(o[2 * i + e]);
-                        }
-                    stsm4t(st + L::kY + tile<YNB>(16 * m + tok_l, col_l), o);
-                }
-                __syncwarp();
-                Tin *to = half ? dlo : dv;
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const int tok = 16 * m + (lane >> 1);
-                    uint4 o;
-                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
-                                 : "r"(st + L::kY + tile<YNB>(tok, 2 * warp + (lane & 1))) : "memory");
-                    if (tok < n_tok) *reinterpret_cast<uint4 *>(to + (t + tok) * ys + 8 * (lane & 1)) = o;
-                }
-            }
+        } else {
+            put_terms(dv + t * ys, dlo + t * ys, ys, n_tok, X, base + L::kOwn + warp * L::own);
         }
         if (r + L::stages < chunks) bar_arrive(empty + r % L::stages, L::meet);
     }

@@ -41,6 +41,10 @@ __device__ __forceinline__ void stsm4t(uint32_t a, const uint32_t (&r)[4]) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
                  :: "r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
 }
+__device__ __forceinline__ void stsm4(uint32_t a, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};"
+                 :: "r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
 // d += a b: a 16 x 16 (rows g, g + 8; columns 2t, 2t + 1, + 8), b 16 x 8, d 16 x 8 with g = lane / 4, t = lane % 4
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -539,25 +543,76 @@ __device__ __forceinline__ void prepare_chunk(uint32_t k, uint32_t q, unsigned c
     put(r, true);
 }
 
-// A warp's 16 rows of a state to a workspace's [unit][N][N]: as fp32, or for bf16 inputs as two bf16 terms
-// in arrays `second` elements apart.
+// A warp's 16 rows of a state to a workspace's [unit][N][N]: as fp32, or for bf16 inputs as two bf16 terms in arrays
+// `second` elements apart, in whole 16-byte pieces through `at`, 64 N bytes of shared memory of the warp's own. Four bytes
+// per lane straight to memory took 8 x 1024 tokens of 12 heads 258 us for the whole backward against 246 (N = 64), and
+// seven packed sequences of 8 heads 525 against 532 (N = 128).
 template <bool F32, int NN>
-__device__ __forceinline__ void keep_state(void *ws, long long second, long long unit, int row, const float (&S)[NN / 8][4]) {
-    const int gr = (threadIdx.x & 31) >> 2, tc = threadIdx.x & 3;
-    const size_t at = (size_t(unit) * NN + row + gr) * NN + 2 * tc;
+__device__ __forceinline__ void keep_state(void *ws, long long second, long long unit, int row, const float (&S)[NN / 8][4], uint32_t at) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (F32) {
+        float *to = static_cast<float *>(ws) + (size_t(unit) * NN + row + (lane >> 2)) * NN + 2 * (lane & 3);
 #pragma unroll
-    for (int n = 0; n < NN / 8; ++n)
+        for (int n = 0; n < NN / 8; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            if constexpr (F32) {
-                *reinterpret_cast<float2 *>(static_cast<float *>(ws) + at + 8 * e * NN + 8 * n) = make_float2(S[n][2 * e], S[n][2 * e + 1]);
-            } else {
-                uint32_t r[2];
-                split2<2>(S[n][2 * e], S[n][2 * e + 1], r);
-                __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(ws) + at + 8 * e * NN + 8 * n;
-                *reinterpret_cast<uint32_t *>(to) = r[0];
-                *reinterpret_cast<uint32_t *>(to + second) = r[1];
+            for (int e = 0; e < 2; ++e) *reinterpret_cast<float2 *>(to + 8 * e * NN + 8 * n) = make_float2(S[n][2 * e], S[n][2 * e + 1]);
+        return;
+    }
+    constexpr int TERM = 16 * NN * 2, PER_ROW = NN / 8;
+    __syncwarp();
+#pragma unroll
+    for (int n = 0; n < NN / 8; n += 2) {
+        uint32_t r[2][4];           // [term][rows g, g + 8 of one tile, of the next]
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t t[2];
+            split2<2>(S[n + (i >> 1)][2 * (i & 1)], S[n + (i >> 1)][2 * (i & 1) + 1], t);
+            r[0][i] = t[0];
+            r[1][i] = t[1];
+        }
+#pragma unroll
+        for (int z = 0; z < 2; ++z) stsm4(at + z * TERM + tile<NN * 2>(lane & 15, n + (lane >> 4)), r[z]);
+    }
+    __syncwarp();
+    __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(ws) + (size_t(unit) * NN + row) * NN;
+#pragma unroll
+    for (int z = 0; z < 2; ++z)
+#pragma unroll
+        for (int i = 0; i < NN / 16; ++i) {
+            const int r = (32 * i + lane) / PER_ROW, c = lane % PER_ROW;
+            uint32_t u[4];
+            ld_v4(u, at + z * TERM + tile<NN * 2>(r, c));
+            *reinterpret_cast<uint4 *>(to + z * second + r * NN + 8 * c) = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+}
+// X^T of a warp (16 value channels, 32 tokens) as two bf16 terms, to rows of tokens `stride` elements apart; through
+// `at` as above.
+__device__ __forceinline__ void put_terms(__nv_bfloat16 *first, __nv_bfloat16 *second, size_t stride, int n_tok, float (&X)[4][4], uint32_t at) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int z = 0; z < 2; ++z)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float *x = &X[2 * m + (i >> 1)][2 * (i & 1)];
+                o[i] = pack(x[0], x[1]);
+                x[0] -= lo_f(o[i]);             // what the rounding leaves
+                x[1] -= hi_f(o[i]);
             }
+            stsm4t(at + z * 1024 + block(16 * m + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1), o);
+        }
+    __syncwarp();
+#pragma unroll
+    for (int z = 0; z < 2; ++z)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const int tok = 16 * m + (lane >> 1);
+            uint32_t u[4];
+            ld_v4(u, at + z * 1024 + block(tok, lane & 1));
+            if (tok < n_tok) *reinterpret_cast<uint4 *>((z ? second : first) + tok * stride + 8 * (lane & 1)) = make_uint4(u[0], u[1], u[2], u[3]);
         }
 }
 

@@ -30,7 +30,9 @@ struct Layout {
     // GROUPS chunks being prepared, one at work, and the rest loading: what two CTAs of N = 64 bf16 with two
     // groups, or one of the others, have room (and named barriers) for
     static constexpr int stages = F32 ? (NN == 64 ? 6 : 3) : (NN == 64 && GROUPS == 2 ? 5 : 6);
-    static constexpr int total = stages * stage + GROUPS * int(sizeof(PrepScratch));
+    static constexpr int own = STATES && !F32 ? 64 * NN : 0;           // bytes of each state warp's own
+    static constexpr int kOwn = stages * stage, kPrep = kOwn + RW * own;
+    static constexpr int total = kPrep + GROUPS * int(sizeof(PrepScratch));
     static constexpr int threads = RW * 32 + GROUPS * kGroup, meet = RW * 32 + kGroup;
 };
 
@@ -88,7 +90,7 @@ __device__ __forceinline__ void forward_sweep(const DeltaArgs &p, unsigned block
 
     if (threadIdx.x >= RW * 32) {           // ---- preparing warps: group g takes chunks g, g + GROUPS, ... ----
         const int group = (threadIdx.x - RW * 32) / kGroup, tid = (threadIdx.x - RW * 32) % kGroup;
-        PrepScratch *ps = reinterpret_cast<PrepScratch *>(sm + L::stages * L::stage) + group;
+        PrepScratch *ps = reinterpret_cast<PrepScratch *>(sm + L::kPrep) + group;
         RowLoader<NN, F32> k(p.k, t0 + group * C, (long long)hk * NN, p.ks, tid), q(p.q, t0 + group * C, (long long)hk * NN, p.qs, tid);
         RowLoader<RW * 16, F32> v(p.v, t0 + group * C, (long long)h * NN + row0, p.vs, tid);
         Gate<F32> gate, next{};
@@ -133,7 +135,7 @@ __device__ __forceinline__ void forward_sweep(const DeltaArgs &p, unsigned block
     const size_t ys = size_t(p.H) * NN;
     Tin *y = static_cast<Tin *>(STATES ? p.keep_E : p.y) + size_t(h) * NN + row;
     [[maybe_unused]] const long long slot0 = delta_slot(t0, s);
-    // y or E (bf16, tokens t ..) from its fragments through the values' place (this warp's own columns) to whole
+    // y (bf16, tokens t ..) from its fragments through the values' place (this warp's own columns) to whole
     // 32-byte pieces
     auto put = [&](Tin *to, uint32_t st, int n_tok, const uint32_t (&r)[2][4]) {
         __syncwarp();
@@ -185,7 +187,7 @@ __device__ __forceinline__ void forward_sweep(const DeltaArgs &p, unsigned block
                 }
         }
         if constexpr (STATES) {         // what the grads' chunks of 64 tokens start from
-            if (c % 2 == 0) keep_state<F32, NN>(p.keep_S, p.keep_second, (slot0 + c / 2) * p.H + h, row, S);
+            if (c % 2 == 0) keep_state<F32, NN>(p.keep_S, p.keep_second, (slot0 + c / 2) * p.H + h, row, S, base + L::kOwn + warp * L::own);
         }
         bar_sync(full + stage, L::meet);
         // X^T = S K^T, Y^T = S Q^T
@@ -382,23 +384,15 @@ __device__ __forceinline__ void forward_sweep(const DeltaArgs &p, unsigned block
                     const int i = 8 * n + 2 * tc + (e & 1);
                     if (i < n_tok) y[(t + i) * ys + gr + 8 * (e >> 1)] = Y[n][e];
                 }
+        } else if constexpr (STATES) {
+            put_terms(y + t * ys, y + t * ys + p.keep_lo, ys, n_tok, Y, base + L::kOwn + warp * L::own);
         } else {
+            uint32_t o[2][4];
 #pragma unroll
-            for (int z = 0; z < (STATES ? 2 : 1); ++z) {        // STATES: the errors in two terms
-                uint32_t o[2][4];
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float *v = &Y[2 * m + (i >> 1)][2 * (i & 1)];
-                        o[m][i] = pack(v[0], v[1]);
-                        if constexpr (STATES) {                 // what the rounding leaves
-                            v[0] -= lo_f(o[m][i]);
-                            v[1] -= hi_f(o[m][i]);
-                        }
-                    }
-                put(y + t * ys + z * p.keep_lo, st, n_tok, o);
-            }
+                for (int i = 0; i < 4; ++i) o[m][i] = pack(Y[2 * m + (i >> 1)][2 * (i & 1)], Y[2 * m + (i >> 1)][2 * (i & 1) + 1]);
+            put(y + t * ys, st, n_tok, o);
         }
         if (c + L::stages < chunks) bar_arrive(empty + stage, L::meet);
     }
