@@ -2,7 +2,9 @@
 //     e = v - exp(g) S k,  S <- exp(g) S + beta e k^T,  y = S q.
 // 16 KB of state in and 16 KB out per head (N = 64) for 28 kflop: bound by HBM bandwidth. One CTA
 // owns one (row, head); a half-warp (N = 64) or a warp (N = 128) covers one row of the state with a
-// float4 per lane, and all of a thread's rows are loaded before any arithmetic.
+// float4 per lane, and all of a thread's rows are loaded before any arithmetic. 250 rows of 40 heads scattered over a
+// pool of 320 slots (333 MB): 58 to 60 us, 5.7 TB/s, of 50.7 us at the rate of a plain copy; CTAs of 128 threads, 6 to 12
+// to an SM, took 61 to 94 us against 61 on the same card.
 // Rows that share a slot: the first of them carries the state through all of the others, in
 // order; the others leave at once. Finding them costs one pass over the slots, which runs under the
 // state's loads.

@@ -269,3 +269,17 @@ def test_select_and_reorder_in_one_graph_on_another_stream(cuda_device):
     assert np.array_equal(out[1].cpu().numpy(), ref[1]) and np.array_equal(out[2].cpu().numpy(), ref[2])
     p = out[1].long()
     assert torch.equal(st, first[:, torch.arange(2, device=cuda_device)[:, None], p])
+
+
+def test_two_selections_at_once(cuda_device):
+    """On two streams, each with its own workspace, many times over: the same as one after the other."""
+    cases = [draw(8, 8, 30_001, "bf16", 91), draw(6, 5, 20_000, "f32", 92)]
+    cases = [(x.to(cuda_device), s.to(cuda_device)) for x, s in cases]
+    ref = [wkv7.beam_select(x, s, 10) for x, s in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        got = [wkv7.beam_select(x, s, 10, stream=t) for (x, s), t in zip(cases, streams)]
+    torch.cuda.synchronize()
+    for g, r in zip(got, ref):
+        assert all(torch.equal(a, b) for a, b in zip(g, r))

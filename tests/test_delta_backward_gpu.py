@@ -208,6 +208,56 @@ def test_repeats_other_streams_and_graphs(cuda_device):
         assert torch.equal(got[n], ref2[n]), n
 
 
+@pytest.mark.parametrize("N,H,Hk", [(64, 8, 4), (64, 3, 3), (128, 4, 2)])
+def test_more_chunks_than_the_gpu_holds_at_once(cuda_device, N, H, Hk):
+    """A CTA of the gradients' kernel takes several chunks, over the ends of sequences, empty ones among them."""
+    lens = [900, 0, 1, 1500, 63, 0, 64, 1400, 65, 0]
+    cu = [0, *np.cumsum(lens).tolist()]
+    d = make((cu[-1],), H, Hk, N, "bf16", seed=61)
+    dy, dS = extra((cu[-1],), len(lens), H, N, "bf16", 62)
+    S0 = state(len(lens), H, N, 63)
+    got = wkv7.delta_backward(*to(d, cuda_device).values(), dy.to(cuda_device), S0.to(cuda_device), dS.to(cuda_device),
+                              qk_norm=True, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=cuda_device))
+    for s, (a, b) in enumerate(zip(cu[:-1], cu[1:])):
+        ref = delta.delta_backward(*(d[n][a:b][None] for n in TOK), S0[s:s + 1], dy[a:b][None], dS[s:s + 1], qk_norm=True)
+        check({**{n: got[n][a:b][None] for n in NAMES}, "dS0": got["dS0"][s:s + 1]}, ref, "bf16")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_nan_stays_in_its_sequence_and_key_head(cuda_device, dt):
+    """A NaN value reaches no gradient of another sequence, nor dv, dg or dbeta of another head."""
+    d = make((3, 150), 4, 2, 64, dt, seed=64)
+    dy, dS = extra((3, 150), 3, 4, 64, dt, 65)
+    run = lambda: wkv7.delta_backward(*to(d, cuda_device).values(), dy.to(cuda_device), None, dS.to(cuda_device),  # noqa: E731
+                                      qk_norm=True)
+    clean = run()
+    d["v"][1, 70, 1, 5] = float("nan")
+    got = run()
+    for n in NAMES + ("dS0",):
+        assert torch.equal(got[n][[0, 2]], clean[n][[0, 2]]), n
+    for n in ("dv", "dg", "dbeta", "dS0"):
+        x, y = (t[n][1] if n == "dS0" else t[n][1].transpose(0, 1) for t in (got, clean))
+        assert torch.equal(x[[0, 2, 3]], y[[0, 2, 3]]), n
+    for n in ("dq", "dk"):
+        assert torch.equal(got[n][1, :, 1], clean[n][1, :, 1]), n
+    assert not torch.isfinite(got["dbeta"][1, 70, 1])
+
+
+def test_two_calls_at_once(cuda_device):
+    """On two streams, each with its own workspace: the same bits as one after the other."""
+    a, b = (to(make((4, 500), 6, 3, 64, "bf16", seed=s), cuda_device) for s in (66, 67))
+    dy = extra((4, 500), 4, 6, 64, "bf16", 68)[0].to(cuda_device)
+    ref = [wkv7.delta_backward(*x.values(), dy, qk_norm=True) for x in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = [wkv7.delta_backward(*x.values(), dy, qk_norm=True, stream=s) for x, s in zip((a, b), streams)]
+    torch.cuda.synchronize()
+    for g, r in zip(got, ref):
+        for n in NAMES + ("dS0",):
+            assert torch.equal(g[n], r[n]), n
+
+
 def test_training_step_follows_the_oracle(cuda_device):
     """Forward and backward as a step uses them: a loss on y and the state, split over two calls with
     the state and its gradient handed between them, equals the oracle's gradients of one pass."""

@@ -137,6 +137,52 @@ def test_forward_nan_stays_in_its_sequence_and_head(cuda_device):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [64, 128])
+@pytest.mark.parametrize("t", [0, 45, 99])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_forward_inputs_that_are_not_finite(cuda_device, bad, t, N, dt):
+    """Each reaches its own token and later ones of what it belongs to, and nothing else."""
+    d = make((2, 100), 4, 2, N, dt, seed=17)
+    ref, S_ref = wkv7.delta_forward(*to(d, cuda_device).values(), qk_norm=True)
+    for name, heads in (("q", [2, 3]), ("k", [2, 3]), ("v", [2]), ("g", [2]), ("beta", [2])):
+        x = {n: v.clone() for n, v in d.items()}
+        if name in "qk":
+            x[name][1, t, 1, 7] = bad
+        elif name == "v":
+            x[name][1, t, 2, 7] = bad
+        else:
+            x[name][1, t, 2] = bad
+        y, S = wkv7.delta_forward(*to(x, cuda_device).values(), qk_norm=True)
+        other = [h for h in range(4) if h not in heads]
+        assert torch.equal(y[0], ref[0]) and torch.equal(S[0], S_ref[0]), name
+        assert torch.equal(y[1][:, other], ref[1][:, other]) and torch.equal(S[1, other], S_ref[1, other]), name
+        mine, was = y[1][:, heads], ref[1][:, heads]
+        for part in ((mine[:t], was[:t]), *([(mine[t + 1:], was[t + 1:])] if name == "q" else [])):
+            assert float((part[0] - part[1]).abs().max() if part[0].numel() else 0) <= Y_TOL[dt] * float(was.abs().max()), name
+        if name == "q":
+            assert not torch.isfinite(mine[t]).any()
+            assert torch.equal(S[1], S_ref[1])
+        elif name == "v":
+            assert not torch.isfinite(mine[t:, :, 7]).any() and not torch.isfinite(S[1, 2, 7]).any()
+            mine, was = (z[..., [i for i in range(N) if i != 7]] for z in (mine, was))
+            assert float((mine - was).abs().max()) <= Y_TOL[dt] * float(was.abs().max())
+        else:
+            assert not torch.isfinite(mine[t:]).any() and not torch.isfinite(S[1, heads]).any()
+
+
+def test_forward_two_calls_at_once(cuda_device):
+    a, b = (to(make((4, 500), 6, 3, 64, "bf16", seed=s), cuda_device) for s in (18, 19))
+    ref = [wkv7.delta_forward(*x.values(), qk_norm=True) for x in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = [wkv7.delta_forward(*x.values(), qk_norm=True, stream=s) for x, s in zip((a, b), streams)]
+    torch.cuda.synchronize()
+    for g, r in zip(got, ref):
+        assert torch.equal(g[0], r[0]) and torch.equal(g[1], r[1])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_forward_strided_rows(cuda_device, dt):
     """q, k and v as views of one projection's output, rows wider than their own heads."""
     H, Hk, N, B, T = 4, 2, 64, 2, 75
