@@ -1,8 +1,10 @@
 // One token of the gated delta rule for every row of a batch, against a pool of fp32 states:
 //     e = v - exp(g) S k,  S <- exp(g) S + beta e k^T,  y = S q.
 // 16 KB of state in and 16 KB out per head (N = 64) for 28 kflop: bound by HBM bandwidth. One CTA
-// owns one (row, head); a half-warp (N = 64) or a warp (N = 128) covers one row of the state with a
-// float4 per lane, and all of a thread's rows are loaded before any arithmetic. 250 rows of 40 heads scattered over a
+// owns 16 KB, a (row, head) at N = 64 and a quarter of one at N = 128; a half-warp (N = 64) or a warp (N = 128) covers one
+// row of the state with a float4 per lane, and all of a thread's four rows are loaded before any arithmetic. (32 rows of 40
+// heads of N = 128, 168 MB: 28 us against 34 with half a state per CTA and 39 with a whole one, whose 16 rows per thread
+// leave two CTAs to an SM.) 250 rows of 40 heads scattered over a
 // pool of 320 slots (333 MB): 58 to 60 us, 5.7 TB/s, of 50.7 us at the rate of a plain copy; CTAs of 128 threads, 6 to 12
 // to an SM, took 61 to 94 us against 61 on the same card.
 // Rows that share a slot: the first of them carries the state through all of the others, in
@@ -17,12 +19,13 @@ namespace {
 __device__ __forceinline__ void store1(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store1(__nv_bfloat16 *p, float x) { *p = __float2bfloat16(x); }
 
-template <class Tin, int NN, int THREADS>
+template <class Tin, int NN, int THREADS, int PARTS>
 __global__ void __launch_bounds__(THREADS) delta_step_kernel(const DeltaArgs p) {
-    constexpr int CL = NN / 4, RS = THREADS / CL, RPT = NN / RS;
-    const int h = blockIdx.x % unsigned(p.H), hk = h / (p.H / p.Hk);
-    int b = blockIdx.x / unsigned(p.H);
-    const int c4 = threadIdx.x % CL, rbase = threadIdx.x / CL;
+    constexpr int CL = NN / 4, RS = THREADS / CL, ROWS = NN / PARTS, RPT = ROWS / RS;
+    const int part = blockIdx.x % PARTS;                   // of the state's rows, which never meet
+    const int h = blockIdx.x / PARTS % unsigned(p.H), hk = h / (p.H / p.Hk);
+    int b = blockIdx.x / PARTS / unsigned(p.H);
+    const int c4 = threadIdx.x % CL, rbase = part * ROWS + threadIdx.x / CL;
     const Tin *q = static_cast<const Tin *>(p.q) + hk * NN + 4 * c4, *k = static_cast<const Tin *>(p.k) + hk * NN + 4 * c4;
     const Tin *v = static_cast<const Tin *>(p.v) + h * NN;
     const Tin *g = static_cast<const Tin *>(p.g) + h, *beta = static_cast<const Tin *>(p.beta) + h;
@@ -34,7 +37,7 @@ __global__ void __launch_bounds__(THREADS) delta_step_kernel(const DeltaArgs p) 
     };
     const int slot = p.slots ? p.slots[b] : b;
     if (slot < 0 || slot >= p.n_slots) {        // padding: uniform over the CTA
-        for (int i = threadIdx.x; i < NN; i += THREADS) store1(y + size_t(b) * p.H * NN + i, 0.f);
+        for (int i = threadIdx.x; i < ROWS; i += THREADS) store1(y + size_t(b) * p.H * NN + part * ROWS + i, 0.f);
         return;
     }
     float *S = p.S + (size_t(slot) * p.H + h) * NN * NN;
@@ -97,8 +100,8 @@ __global__ void __launch_bounds__(THREADS) delta_step_kernel(const DeltaArgs p) 
 template <class Tin>
 cudaError_t launch_t(const DeltaArgs &p) {
     const unsigned grid = unsigned(p.B) * unsigned(p.H);
-    if (p.N == 128) delta_step_kernel<Tin, 128, 256><<<grid, 256, 0, p.stream>>>(p);
-    else delta_step_kernel<Tin, 64, 256><<<grid, 256, 0, p.stream>>>(p);
+    if (p.N == 128) delta_step_kernel<Tin, 128, 256, 4><<<4 * grid, 256, 0, p.stream>>>(p);
+    else delta_step_kernel<Tin, 64, 256, 1><<<grid, 256, 0, p.stream>>>(p);
     return cudaGetLastError();
 }
 

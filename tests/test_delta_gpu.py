@@ -326,6 +326,21 @@ def test_step_rows_that_share_a_slot_follow_one_another(cuda_device):
         check(y[rows][None], S[s:s + 1], yr, Sr, "f32")
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_step_rows_that_share_a_slot_at_head_size_128(cuda_device, dt):
+    B, H, N = 37, 2, 128
+    d = make((B,), H, 1, N, dt, seed=35)
+    slots = torch.tensor([(3 * b) % 7 - 1 for b in range(B)], dtype=torch.int32)
+    S0 = state(6, H, N, 13)
+    S = S0.to(cuda_device)
+    y = wkv7.delta_step(*to(d, cuda_device).values(), S, qk_norm=True, slots=slots.to(cuda_device))
+    assert bool(torch.all(y[slots.to(cuda_device) < 0] == 0))
+    for s in range(6):
+        rows = (slots == s).nonzero().flatten().tolist()
+        yr, Sr = delta.delta_recurrence(*(d[n][rows][None] for n in TOK), S0[s:s + 1], qk_norm=True)
+        check(y[rows][None], S[s:s + 1], yr, Sr, dt)
+
+
 def test_steps_equal_the_forward(cuda_device):
     """Prefill, then 20 steps from a captured graph, against one forward over all tokens."""
     B, T, H, N = 3, 60, 4, 64
