@@ -905,7 +905,7 @@ size_t wkv7_delta_backward_workspace_bytes(int B, int T, int H, int Hk, int N, w
     wkv7_delta_opts o;
     size_t rows = 0;
     if (delta_args(B, T, H, Hk, N, dt, opts_in, o, rows) != WKV7_OK || rows == 0) return 0;
-    return wkv7::delta_backward_workspace(rows, B, H, N, dt);
+    return wkv7::delta_backward_workspace(rows, B, H, Hk, N, dt);
 }
 
 wkv7_status wkv7_delta_backward(int B, int T, int H, int Hk, int N, wkv7_dtype dt, const void *q, const void *k,
@@ -918,7 +918,7 @@ wkv7_status wkv7_delta_backward(int B, int T, int H, int Hk, int N, wkv7_dtype d
     wkv7_status st = delta_args(B, T, H, Hk, N, dt, opts_in, o, rows);
     if (st != WKV7_OK) return st;
     if ((rows / 64 + B) * static_cast<size_t>(Hk) > size_t(INT_MAX)) return fail(WKV7_ERR_ARG, "sizes overflow");
-    const size_t need = rows ? wkv7::delta_backward_workspace(rows, B, H, N, dt) : 0;
+    const size_t need = rows ? wkv7::delta_backward_workspace(rows, B, H, Hk, N, dt) : 0;
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(WKV7_ERR_WORKSPACE, "workspace of %zu bytes required, %zu given", need, workspace ? workspace_bytes : 0);
     const size_t kw = size_t(Hk) * N, vw = size_t(H) * N, el = elem_bytes(dt), gb = rows * H * el;

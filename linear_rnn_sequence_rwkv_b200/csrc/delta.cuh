@@ -36,13 +36,16 @@ struct DeltaArgs {
     void *keep_dlo;         // workspace, bf16: the second term of dv
     void *keep_S, *keep_dS; // workspace: the state a chunk of 64 tokens starts from and its last state's gradient
     long long keep_second;  // bf16: elements from their first terms to the second
+    float *keep_parts;      // workspace: dq, then dk, of each part of the value heads, parts_step elements each
+    long long parts_step;
+    int group;              // value heads of a key head
     cudaStream_t stream;
 };
 
 cudaError_t launch_delta_forward(const DeltaArgs &p);
 cudaError_t launch_delta_step(const DeltaArgs &p);
 cudaError_t launch_delta_backward(const DeltaArgs &p);      // both kernels of the backward
-size_t delta_backward_workspace(size_t rows, int B, int H, int N, wkv7_dtype dt);
+size_t delta_backward_workspace(size_t rows, int B, int H, int Hk, int N, wkv7_dtype dt);
 
 // Chunks of 64 tokens are numbered over all sequences so that each has a place of its own without a pass over
 // the lengths: sequence s starts at number (first row) / 64 + s, and there are at most rows / 64 + B.

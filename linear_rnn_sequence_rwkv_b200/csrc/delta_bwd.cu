@@ -15,7 +15,8 @@
 //          dG_i = sum_{j<i} beta_j z_ij - beta_i sum_{j>i} z_ji + q_i.(qin dY S)_i - k_i.(kin dX S)_i
 //          dg_t = sum_{i >= t} dG_i + sum_{j < t} beta_j tail_j + exp(G_C) <S, dS'>
 //      (rk, sq: 1 / |k| and scale / |q|; with unit keys dk = rk dK - k^ (k^.rk dK), and q alike).
-//      The value heads of one key head are summed in the same accumulators, in order.
+//      The value heads of one key head are summed in the same accumulators, in order; where that would leave SMs idle
+//      they go to several CTAs, whose sums delta_grad_sum_kernel adds up in order.
 // Precision: the chain of dS keeps three bf16 terms wherever a state or its gradient is read or written. For
 // outputs in bf16, everything computed (E, dX, S, dS', n, o) enters the sums in two terms, 16 bits: dg is a
 // difference of large sums and would show a single term's rounding several times over.
@@ -295,10 +296,11 @@ __global__ void __launch_bounds__(RW * 32 + GROUPS * kGroup, (!F32 && NN == 64 &
 
 constexpr int GC = 64, GT = 512;        // tokens, threads (16 warps: 4 row blocks of 16 by 4 column groups)
 
-// Tokens t0 .. t0 + n - 1 of a sequence, number `slot` of all chunks, and a key head. n = 0: none left.
+// Tokens t0 .. t0 + n - 1 of a sequence, number `slot` of all chunks; a key head, and `heads` of its value heads from
+// `first` on. n = 0: none left.
 struct GradChunk {
     long long t0, slot;
-    int n, hk;
+    int n, hk, first, heads, part;
 };
 struct GradScalars {
     float ghi[GC], glo[GC], rk[GC], sq[GC], beta[GC], kin[GC], qin[GC], kout[GC], out[GC];
@@ -307,7 +309,7 @@ struct GradScalars {
     float ss[GT / 32];
     float whole;
     int near;                       // the chunk's sums of log decays stay within 30 of the middle one
-    GradChunk next;
+    GradChunk chunk[2];             // at work and next, in turn
 };
 
 template <int NN, bool F32>
@@ -439,10 +441,12 @@ __device__ __forceinline__ void eight_at(float (&x)[8], uint32_t at, int term) {
     }
 }
 
-// The first task from `task` on that has tokens: task = (chunk number) * Hk + key head.
-__device__ __forceinline__ GradChunk grad_chunk(const DeltaArgs &p, unsigned &task, unsigned tasks) {
+// The first task from `task` on that has tokens: task = ((chunk number) * Hk + key head) * parts + part, where a key head's
+// value heads go to `parts` tasks.
+__device__ __forceinline__ GradChunk grad_chunk(const DeltaArgs &p, unsigned &task, unsigned tasks, int parts) {
     for (; task < tasks; task += gridDim.x) {
-        const long long slot = task / unsigned(p.Hk);
+        const unsigned whole = parts == 1 ? task : task / unsigned(parts), number = p.Hk == 1 ? whole : whole / unsigned(p.Hk);
+        const long long slot = number;
         // the sequence of this chunk: the last one that starts at or before it
         int s = 0;
         for (int lo = 0, hi = p.B; lo < hi;) {
@@ -459,22 +463,28 @@ __device__ __forceinline__ GradChunk grad_chunk(const DeltaArgs &p, unsigned &ta
         delta_rows(p.cu, p.T, s, t0, t1);
         const long long chunk = slot - delta_slot(t0, s);
         t0 += chunk * GC;
-        if (chunk >= 0 && t0 < t1) return {t0, slot, int(min((long long)GC, t1 - t0)), int(task % unsigned(p.Hk))};
+        if (chunk >= 0 && t0 < t1) {
+            const int hk = whole - number * p.Hk, part = task - whole * parts, n = int(min((long long)GC, t1 - t0));
+            if (parts == 1) return {t0, slot, n, hk, hk * p.group, p.group, 0};
+            const int from = p.group * part / parts;
+            return {t0, slot, n, hk, hk * p.group + from, p.group * (part + 1) / parts - from, part};
+        }
     }
-    return {0, 0, 0, 0};
+    return {};
 }
 
-template <int NN, bool F32>
-__global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p, unsigned tasks) {
+// SPLIT: a key head's value heads are divided into n_parts (one otherwise).
+template <int NN, bool F32, bool SPLIT>
+__global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p, unsigned tasks, int n_parts) {
     using L = GradLayout<NN, F32>;
     using Tin = std::conditional_t<F32, float, __nv_bfloat16>;
     constexpr int TI = L::TI, TE = L::TE, DW = L::DW, NB = NN * 2, YNB = DW * 2, CT = NN / 32, CW = NN / 4;
+    const int parts = SPLIT ? n_parts : 1;
     extern __shared__ __align__(1024) unsigned char sm[];
     GradScalars *sc = reinterpret_cast<GradScalars *>(sm + L::total - sizeof(GradScalars));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tc = lane & 3;
     constexpr int scalar_warp = 12;     // the one with the fewest products (wr = 0, wc = 3) sees to the gates
     const int wr = warp & 3, wc = warp >> 2, c0 = wc * CW, j0 = wc * 16;   // rows 16 wr; key channels c0; tokens j0 ..
-    const int group = p.H / p.Hk;
     const Pieces<DW, GC> tok((long long)p.H * NN);
     const Pieces<NN, DW> sta(NN);
     auto load_keys = [&](uint32_t to, const GradChunk &c) {
@@ -496,20 +506,25 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p, un
         }
     };
     unsigned at_task = blockIdx.x;
-    GradChunk cur = grad_chunk(p, at_task, tasks);
-    if (cur.n == 0) return;
+    GradChunk *cur = &sc->chunk[0];         // in shared memory: the registers are full
+    {
+        const GradChunk c = grad_chunk(p, at_task, tasks, parts);
+        if (c.n == 0) return;
+        if (tid == 0) *cur = c;
+        __syncthreads();
+    }
     // of the keys and queries, and of the slice: each moves to the other set and back
     const uint32_t both = 2 * smem_addr(sm) + L::kF;
     uint32_t keys = smem_addr(sm), base = keys;
-    load_keys(keys, cur);
-    if constexpr (L::AHEAD) load_slice(base, cur, cur.hk * group, 0);
+    load_keys(keys, *cur);
+    if constexpr (L::AHEAD) load_slice(base, *cur, cur->first, 0);
     cp_commit();
     while (true) {
-        const long long t0 = cur.t0;
-        const int n = cur.n, hk = cur.hk;
+        const long long t0 = cur->t0;
+        const int n = cur->n;
         float DQ[CT][4] = {}, DK[CT][4] = {};
-        for (int hg = 0; hg < group; ++hg) {
-            const int h = hk * group + hg;
+        for (int hg = 0; hg < (SPLIT ? cur->heads : p.group); ++hg) {
+            const int h = cur->first + hg;
             float A[2][4] = {}, B[2][4] = {}, QK[2][4] = {}, KK[2][4] = {}, aq[CT][4] = {}, ak[CT][4] = {}, ao[CT][4] = {};
             float ss = 0.f;
             for (int sl = 0; sl < NN / DW; ++sl) {
@@ -521,19 +536,19 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p, un
 #pragma unroll
                         for (int e = 0; e < 2; ++e) gates[e].load(p.g, p.beta, (t0 + 2 * lane + e) * p.H + h, 2 * lane + e < n);
                     }
-                    if (hg + 1 < group) {
+                    if (hg + 1 < (SPLIT ? cur->heads : p.group)) {
                         // the keys and queries stay where they are
-                        load_slice(both - base, cur, h + 1, 0);
+                        load_slice(both - base, *cur, h + 1, 0);
                     } else {
-                        const GradChunk next = grad_chunk(p, at_task += gridDim.x, tasks);
-                        if (tid == 0) sc->next = next;
+                        const GradChunk next = grad_chunk(p, at_task += gridDim.x, tasks, parts);
+                        if (tid == 0) (cur == &sc->chunk[0] ? sc->chunk[1] : sc->chunk[0]) = next;
                         if (next.n) {
                             load_keys(both - keys, next);
-                            load_slice(both - base, next, next.hk * group, 0);
+                            load_slice(both - base, next, next.first, 0);
                         }
                     }
                 } else {
-                    load_slice(base, cur, h, sl);
+                    load_slice(base, *cur, h, sl);
                 }
                 cp_commit();
                 if (sl == 0) {              // what needs only keys, queries and gates, while the slice is on its way
@@ -925,8 +940,12 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p, un
             for (int e = 0; e < 4; e += 2) {
                 const int i = 16 * wr + gr + 4 * e;
                 if (i >= n) continue;
-                const long long at = ((t0 + i) * p.Hk + hk) * NN + c0 + 8 * m + 2 * tc;
-                if constexpr (F32) {
+                const long long at = ((t0 + i) * p.Hk + cur->hk) * NN + c0 + 8 * m + 2 * tc;
+                if constexpr (SPLIT) {
+                    float *to = p.keep_parts + cur->part * 2 * p.parts_step + at;
+                    *reinterpret_cast<float2 *>(to) = make_float2(DQ[m][e], DQ[m][e + 1]);
+                    *reinterpret_cast<float2 *>(to + p.parts_step) = make_float2(DK[m][e], DK[m][e + 1]);
+                } else if constexpr (F32) {
                     *reinterpret_cast<float2 *>(static_cast<float *>(p.dq) + at) = make_float2(DQ[m][e], DQ[m][e + 1]);
                     *reinterpret_cast<float2 *>(static_cast<float *>(p.dk) + at) = make_float2(DK[m][e], DK[m][e + 1]);
                 } else {
@@ -935,9 +954,29 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p, un
                 }
             }
         if constexpr (!L::AHEAD) return;
-        cur = sc->next;
-        if (cur.n == 0) return;
+        cur = cur == &sc->chunk[0] ? &sc->chunk[1] : &sc->chunk[0];
+        if (cur->n == 0) return;
         keys = both - keys;
+    }
+}
+
+// The sum of the parts of dq and dk, in order.
+template <int NN, bool F32>
+__global__ void __launch_bounds__(256) delta_grad_sum_kernel(const DeltaArgs p, unsigned tasks, int parts) {
+    unsigned task = blockIdx.x;
+    const GradChunk c = grad_chunk(p, task, tasks, 1);
+    for (int i = threadIdx.x; i < c.n * (NN / 2); i += 256) {
+        const int which = i / (c.n * (NN / 4)), j = i % (c.n * (NN / 4));
+        const long long at = ((c.t0 + j / (NN / 4)) * p.Hk + c.hk) * NN + 4 * (j % (NN / 4));
+        const float *from = p.keep_parts + which * p.parts_step + at;
+        float4 x = *reinterpret_cast<const float4 *>(from);
+        for (int k = 1; k < parts; ++k) {
+            const float4 y = *reinterpret_cast<const float4 *>(from + k * 2 * p.parts_step);
+            x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+        }
+        void *to = which ? p.dk : p.dq;
+        if constexpr (F32) *reinterpret_cast<float4 *>(static_cast<float *>(to) + at) = x;
+        else *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(to) + at) = make_uint2(pack(x.x, x.y), pack(x.z, x.w));
     }
 }
 
@@ -949,16 +988,21 @@ cudaError_t allow_dynamic_smem(const void *kernel, int bytes);
 
 namespace {
 
+// Into how many parts the value heads of a key head go: one, in the same accumulators, where the chunks and key heads fill
+// the SMs; else as many as do. One sequence of 173 tokens with 36 heads on 4 key heads (fp32, N = 128)
+// takes 188 us for the whole backward so and 573 in one part; 14 sequences of 3 tokens, 27 heads on one: 159 and 544.
+int parts_of(long long slots, int H, int Hk) {
+    const long long whole = slots * Hk;
+    return whole >= 148 ? 1 : int(std::max(1ll, std::min<long long>(H / Hk, 148 / whole)));
+}
+
 template <int NN, int RW, bool F32, int GROUPS>
 cudaError_t launch_t(const DeltaArgs &p, long long slots) {
     constexpr int fwd_bytes = Layout<NN, RW, F32, true, GROUPS>::total, rev_bytes = RevLayout<NN, RW, F32, GROUPS>::total;
     constexpr int sweep_bytes = fwd_bytes > rev_bytes ? fwd_bytes : rev_bytes;
     using G = GradLayout<NN, F32>;
     const void *sweeps = reinterpret_cast<const void *>(delta_sweeps_kernel<NN, RW, F32, GROUPS>);
-    const void *grad = reinterpret_cast<const void *>(delta_grad_kernel<NN, F32>);
     cudaError_t e = allow_dynamic_smem(sweeps, sweep_bytes);
-    if (e != cudaSuccess) return e;
-    e = allow_dynamic_smem(grad, G::total);
     if (e != cudaSuccess) return e;
     // Together where that fills SMs that one sweep leaves idle (and at N = 128, where a CTA has an SM to itself:
     // 541 us against 584 for seven packed sequences of 8 heads); in turn otherwise, since blocks of the two kinds
@@ -970,8 +1014,15 @@ cudaError_t launch_t(const DeltaArgs &p, long long slots) {
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    const long long tasks = slots * p.Hk;
-    delta_grad_kernel<NN, F32><<<unsigned(G::AHEAD ? std::min(tasks, 148ll) : tasks), GT, G::total, p.stream>>>(p, unsigned(tasks));
+    const int parts = parts_of(slots, p.H, p.Hk);
+    const long long whole = slots * p.Hk, tasks = whole * parts;
+    const auto grad = parts > 1 ? delta_grad_kernel<NN, F32, true> : delta_grad_kernel<NN, F32, false>;
+    e = allow_dynamic_smem(reinterpret_cast<const void *>(grad), G::total);
+    if (e != cudaSuccess) return e;
+    grad<<<unsigned(G::AHEAD ? std::min(tasks, 148ll) : tasks), GT, G::total, p.stream>>>(p, unsigned(tasks), parts);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || parts == 1) return e;
+    delta_grad_sum_kernel<NN, F32><<<unsigned(whole), 256, 0, p.stream>>>(p, unsigned(whole), parts);
     return cudaGetLastError();
 }
 
@@ -979,10 +1030,13 @@ size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-// Per row E (bf16: in two terms) and the second term of dv, per chunk of 64 S and dS (bf16: in two terms).
-size_t delta_backward_workspace(size_t rows, int B, int H, int N, wkv7_dtype dt) {
+// Per row E (bf16: in two terms) and the second term of dv, per chunk of 64 S and dS (bf16: in two terms); dq and dk of
+// each part in fp32 where there are several.
+size_t delta_backward_workspace(size_t rows, int B, int H, int Hk, int N, wkv7_dtype dt) {
     const size_t row = rows * H * N, state = (rows / 64 + B) * H * N * N;
-    return dt == WKV7_BF16 ? 3 * up(row * 2) + 4 * up(state * 2) : up(row * 4) + 2 * up(state * 4);
+    const int parts = parts_of((long long)(rows / 64 + B), H, Hk);
+    const size_t summed = parts > 1 ? size_t(parts) * 2 * rows * Hk * N * 4 : 0;
+    return summed + (dt == WKV7_BF16 ? 3 * up(row * 2) + 4 * up(state * 2) : up(row * 4) + 2 * up(state * 4));
 }
 
 cudaError_t launch_delta_backward(const DeltaArgs &p0) {
@@ -996,6 +1050,9 @@ cudaError_t launch_delta_backward(const DeltaArgs &p0) {
     p.keep_S = ws;
     p.keep_dS = ws + (p.dt == WKV7_BF16 ? 2 : 1) * state;
     p.keep_second = (long long)(state / el);
+    p.keep_parts = reinterpret_cast<float *>(ws + (p.dt == WKV7_BF16 ? 4 : 2) * state);
+    p.parts_step = (long long)rows * p.Hk * p.N;
+    p.group = p.H / p.Hk;
     if (p.dt == WKV7_F32) return p.N == 64 ? launch_t<64, 4, true, 2>(p, slots) : launch_t<128, 4, true, 2>(p, slots);
     if (p.N == 128) return launch_t<128, 4, false, 2>(p, slots);
     return (long long)p.B * p.H <= 37 ? launch_t<64, 2, false, 3>(p, slots) : launch_t<64, 4, false, 2>(p, slots);     // as forward, twice the blocks

@@ -101,12 +101,15 @@ def test_backward_refusals(lib):
 
 def test_backward_workspace(lib):
     """E in two bf16 terms and dv's second per row and head, two states in two bf16 terms each per chunk
-    of 64 (one more per sequence); fp32 keeps E and the states as they are."""
+    of 64 (one more per sequence); fp32 keeps E and the states as they are. Where chunks and key heads are
+    fewer than the SMs, the value heads of a key head go to several parts, each with dq and dk in fp32."""
     f = lib.wkv7_delta_backward_workspace_bytes
-    assert f(2, 100, 4, 2, 64, 1, None) == 3 * 200 * 4 * 64 * 2 + 4 * 5 * 4 * 4096 * 2
-    assert f(2, 100, 4, 2, 64, 0, None) == 200 * 4 * 64 * 4 + 2 * 5 * 4 * 4096 * 4
+    assert f(2, 100, 4, 2, 64, 1, None) == 3 * 200 * 4 * 64 * 2 + 4 * 5 * 4 * 4096 * 2 + 2 * 2 * 200 * 2 * 64 * 4
+    assert f(2, 100, 4, 2, 64, 0, None) == 200 * 4 * 64 * 4 + 2 * 5 * 4 * 4096 * 4 + 2 * 2 * 200 * 2 * 64 * 4
+    assert f(2, 100, 4, 4, 64, 1, None) == 3 * 200 * 4 * 64 * 2 + 4 * 5 * 4 * 4096 * 2
+    assert f(37, 100, 8, 2, 64, 0, None) == 3700 * 8 * 64 * 4 + 2 * 94 * 8 * 4096 * 4
     o = _opts(cu_seqlens=BASE)
-    assert f(3, 100, 4, 2, 128, 1, ctypes.byref(o)) == 3 * 100 * 4 * 128 * 2 + 4 * 4 * 4 * 16384 * 2
+    assert f(3, 100, 4, 2, 128, 1, ctypes.byref(o)) == 3 * 100 * 4 * 128 * 2 + 4 * 4 * 4 * 16384 * 2 + 2 * 2 * 100 * 2 * 128 * 4
     assert f(2, 0, 4, 2, 64, 1, None) == 0 and f(2, 10, 3, 2, 64, 1, None) == 0
 
 
