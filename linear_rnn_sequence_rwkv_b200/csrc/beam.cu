@@ -11,9 +11,9 @@
 // complement of the index, so that keys never tie and equal values go to the lowest index.
 // beam_pick_kernel: one CTA per request joins the segments' sums in fp64, merges the sorted lists of a row and
 // then those of the rows.
-// 64 requests of 8 beams over 50277 bf16 logits (51.5 MB): 33 us, of which the segments 24 (2.1 TB/s; issue 58 %, 799
-// instructions per warp of 1280 logits, 200 of them exponentials); 28 us where rows are aligned to 16 bytes. One
-// request of 4 beams over 65536 fp32 logits: 8.3 us.
+// 64 requests of 8 beams over 50277 bf16 logits (51.5 MB): 29 us, of which the segments 24 (2.1 TB/s; issue 62 %, 715
+// instructions per warp of 1280 logits, 140 of them for the exponentials); 27 us where rows are aligned to 16 bytes.
+// One request of 4 beams over 65536 fp32 logits: 8.4 us.
 #include "beam.cuh"
 
 #include <cuda_bf16.h>
@@ -49,29 +49,50 @@ __device__ __forceinline__ unsigned long long make_key(float x, uint32_t index) 
     return o ? ((unsigned long long)o << 32) | (0xffffffffu - index) : 0ull;
 }
 
-// 16 bytes from p, which lies `shift` elements behind a 16-byte boundary: the two aligned vectors
-// around it, shifted together. Rows of an odd vocabulary start anywhere; equal rows must be cut into
-// the same vectors all the same, so that their sums, and with them ties between beams, come out equal.
-template <class Tin>
-__device__ __forceinline__ uint4 load_shifted(const Tin *p, int shift) {
-    const uint4 *a = reinterpret_cast<const uint4 *>(p - shift);
-    if (shift == 0) return __ldg(a);
-    const uint4 u = __ldg(a), v = __ldg(a + 1);
-    uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-    const int bytes = shift * int(sizeof(Tin));
-    if (bytes & 8) {
+// A thread's vectors from a row that starts SHIFT elements behind a 16-byte boundary: each is two aligned ones, shifted
+// together. Rows of an odd vocabulary start anywhere; equal rows must be cut into the same vectors all the same, so that
+// their sums, and with them ties between beams, come out equal. Vectors from behind `most` are left out.
+template <class Tin, int NV, int STEP, int SHIFT>
+__device__ __forceinline__ void load_shifted(uint4 (&v)[NV], const Tin *row, int at, int most) {
+    constexpr int q = SHIFT * int(sizeof(Tin)) / 4, half = SHIFT * int(sizeof(Tin)) % 4;
 #pragma unroll
-        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-    }
-    if (bytes & 4) {
+    for (int j = 0; j < NV; ++j) {
+        const int i = at + j * STEP;
+        if (i > most) continue;
+        const uint4 *a = reinterpret_cast<const uint4 *>(row + i - SHIFT);
+        if constexpr (SHIFT == 0) {
+            v[j] = __ldg(a);
+        } else {
+            const uint4 x = __ldg(a), y = __ldg(a + 1);
+            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            uint32_t r[4];
 #pragma unroll
-        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+            for (int k = 0; k < 4; ++k) r[k] = half ? __funnelshift_r(w[k + q], w[min(k + q + 1, 7)], 16) : w[k + q];
+            v[j] = make_uint4(r[0], r[1], r[2], r[3]);
+        }
     }
-    if (bytes & 2) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+}
+template <int NV, int STEP>
+__device__ __forceinline__ void load_row(uint4 (&v)[NV], const float *row, int shift, int at, int most) {
+    switch (shift) {
+        case 0: return load_shifted<float, NV, STEP, 0>(v, row, at, most);
+        case 1: return load_shifted<float, NV, STEP, 1>(v, row, at, most);
+        case 2: return load_shifted<float, NV, STEP, 2>(v, row, at, most);
+        default: return load_shifted<float, NV, STEP, 3>(v, row, at, most);
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <int NV, int STEP>
+__device__ __forceinline__ void load_row(uint4 (&v)[NV], const __nv_bfloat16 *row, int shift, int at, int most) {
+    switch (shift) {
+        case 0: return load_shifted<__nv_bfloat16, NV, STEP, 0>(v, row, at, most);
+        case 1: return load_shifted<__nv_bfloat16, NV, STEP, 1>(v, row, at, most);
+        case 2: return load_shifted<__nv_bfloat16, NV, STEP, 2>(v, row, at, most);
+        case 3: return load_shifted<__nv_bfloat16, NV, STEP, 3>(v, row, at, most);
+        case 4: return load_shifted<__nv_bfloat16, NV, STEP, 4>(v, row, at, most);
+        case 5: return load_shifted<__nv_bfloat16, NV, STEP, 5>(v, row, at, most);
+        case 6: return load_shifted<__nv_bfloat16, NV, STEP, 6>(v, row, at, most);
+        default: return load_shifted<__nv_bfloat16, NV, STEP, 7>(v, row, at, most);
+    }
 }
 __device__ __forceinline__ void unpack(const uint4 v, float (&x)[4]) {
     x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
@@ -238,12 +259,12 @@ __global__ void __launch_bounds__(kT, NV > 4 ? 5 : 6) beam_part_kernel(const Bea
     const int shift = int((reinterpret_cast<uintptr_t>(base) / sizeof(Tin)) % VW);
     const int most = p.V - VW - (shift ? VW - shift : 0);  // last place from which a whole (shifted) vector may be read
     const int at = split * SEG + tid * VW;                 // V + 65536 fits an int
-    uint4 v[NV];
+    uint4 v[NV] = {};
+    load_row<NV, kT * VW>(v, base, shift, at, most);
+    if (at + (NV - 1) * kT * VW > most) {                  // the row ends here
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int i = at + j * kT * VW;
-        if (i <= most) v[j] = load_shifted(base + i, shift);
-        else v[j] = load_edge(base, i, p.V);
+        for (int j = 0; j < NV; ++j)
+            if (at + j * kT * VW > most) v[j] = load_edge(base, at + j * kT * VW, p.V);
     }
     if (tid == 0) {
         s_floor = 0;
