@@ -685,7 +685,8 @@ def _plain(name, t, shape, dtype, dev):
 
 def _row_stride(name, t, shape, dtype, dev):
     """Elements from one token's row to the next of a tensor whose heads and channels are dense and
-    whose rows are evenly spaced over all leading dimensions (0 for the dense layout)."""
+    whose rows are evenly spaced over all leading dimensions (0 for the dense layout, or a single row).
+    Rows that overlap, as those of an expanded tensor do, are refused."""
     if t.shape != shape or t.dtype != dtype or t.device != dev:
         _wrong(name, t, shape, dtype, dev)
     if t.is_contiguous():
@@ -701,7 +702,11 @@ def _row_stride(name, t, shape, dtype, dev):
         if st != step:
             raise ValueError(f"{name}: its rows are not evenly spaced; make it contiguous")
         step *= n
-    return 0 if row is None else row
+    if row is None:
+        return 0
+    if row < t.shape[-2] * t.shape[-1]:     # an expanded tensor's 0 would read as dense
+        raise ValueError(f"{name}: its rows lie {row} elements apart and overlap; make it contiguous")
+    return row
 
 
 def _delta_args(q, k, v, g, beta, scale, qk_norm, norm_eps, cu_seqlens, lead):
