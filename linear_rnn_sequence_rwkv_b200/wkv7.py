@@ -852,7 +852,9 @@ def beam_select(logits, scores, M, *, finished=None, eos=0, out=None, workspace=
             raise ValueError("logits must be dense over the vocabulary")
         stride = logits.stride(1) if K > 1 else (logits.stride(0) if B > 1 else V)
         if B > 1 and K > 1 and logits.stride(0) != K * stride:
-            raise ValueError("logits: its rows are not evenly spaced")
+            raise ValueError("logits: its rows are not evenly spaced; make it contiguous")
+        if stride < V:                      # an expanded tensor's 0 would read as dense
+            raise ValueError(f"logits: its rows lie {stride} elements apart and overlap; make it contiguous")
     _plain("scores", scores, (B, K), torch.float32, dev)
     if finished is not None:
         _plain("finished", finished, (B, K), torch.bool if finished.dtype == torch.bool else torch.uint8, dev)

@@ -43,3 +43,19 @@ def test_rows_that_overlap():
 def test_one_row_has_no_stride():
     x = torch.zeros(1, 1, 2, 64)
     assert wkv7._row_stride("q", x.expand(1, 1, 2, 64), (1, 1, 2, 64), torch.float32, x.device) == 0
+
+
+@pytest.mark.parametrize("B,K,kept", [(1, 4, (1, 1)), (3, 4, (1, 1)), (3, 1, (1, 1)), (3, 4, (3, 1)), (3, 4, (1, 4))])
+def test_logits_expanded_over_beams_or_requests(B, K, kept):
+    """As in a search's first step, where every beam of a request has the prompt's logits."""
+    x = torch.zeros(*kept, 50, dtype=torch.bfloat16).expand(B, K, 50)
+    with pytest.raises(ValueError, match="logits: its rows"):
+        wkv7.beam_select(x, torch.zeros(B, K), 2)
+
+
+def test_logits_whose_rows_overlap():
+    x = torch.zeros(200).as_strided((2, 3, 50), (30, 10, 1))
+    with pytest.raises(ValueError, match="logits: its rows"):
+        wkv7.beam_select(x, torch.zeros(2, 3), 2)
+    with pytest.raises(ValueError, match="logits: its rows"):
+        wkv7.beam_select(torch.zeros(1, 1, 1).expand(2, 3, 1), torch.zeros(2, 3), 2)
