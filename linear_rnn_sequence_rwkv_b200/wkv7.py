@@ -735,7 +735,10 @@ def _delta_args(q, k, v, g, beta, scale, qk_norm, norm_eps, cu_seqlens, lead):
             raise ValueError("cu_seqlens needs one dimension of at least two entries")
         _plain("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, v.device)
         cu = cu_seqlens.data_ptr()
-    return shape, H, Hk, N, dt, DeltaOpts(0.0 if scale is None else scale, int(qk_norm), norm_eps, cu, qs, ks_, vs)
+    o = DeltaOpts(0.0 if scale is None else scale, int(qk_norm), norm_eps, cu, qs, ks_, vs)
+    if scale is not None and o.scale == 0.0:        # the library's 0 is the default
+        raise ValueError(f"scale={scale} is 0 in fp32; None is 1 / sqrt(N)")
+    return shape, H, Hk, N, dt, o
 
 
 def _like(t):

@@ -59,3 +59,15 @@ def test_logits_whose_rows_overlap():
         wkv7.beam_select(x, torch.zeros(2, 3), 2)
     with pytest.raises(ValueError, match="logits: its rows"):
         wkv7.beam_select(torch.zeros(1, 1, 1).expand(2, 3, 1), torch.zeros(2, 3), 2)
+
+
+@pytest.mark.parametrize("scale", [0, 0.0, -0.0, 1e-60])
+def test_a_scale_of_zero(scale):
+    """The library reads 0 as its default, 1 / sqrt(N): a caller's own zero is not that."""
+    d = _tokens(1, 3)
+    with pytest.raises(ValueError, match="scale"):
+        wkv7.delta_forward(*d.values(), scale=scale)
+    with pytest.raises(ValueError, match="scale"):
+        wkv7.delta_backward(*d.values(), torch.zeros_like(d["v"]), scale=scale)
+    with pytest.raises(ValueError, match="scale"):
+        wkv7.delta_step(*(x[0] for x in d.values()), torch.zeros(3, 4, 64, 64), scale=scale)
