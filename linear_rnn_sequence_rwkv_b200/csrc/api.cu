@@ -811,6 +811,9 @@ wkv7_status wkv7_epilogue_backward(int B, int T, int H, int N, wkv7_dtype dt, co
 
 namespace {
 
+// Whether rows `stride` elements apart stay within what a pointer can reach.
+bool reach_ok(size_t rows, long long stride) { return rows <= (size_t(1) << 56) / static_cast<size_t>(stride); }
+
 // Sizes and options shared by the gated delta rule's entries; fills `opts` (defaults if NULL) and the
 // number of rows.
 wkv7_status delta_args(int B, int T, int H, int Hk, int N, wkv7_dtype dt, const wkv7_delta_opts *opts_in,
@@ -842,10 +845,12 @@ wkv7_status delta_args(int B, int T, int H, int Hk, int N, wkv7_dtype dt, const 
     tok = rows;
     if (!mul_ok(tok, H) || !mul_ok(tok, N) || tok > (size_t(1) << 40) || rows > (size_t(1) << 40))
         return fail(WKV7_ERR_ARG, "sizes overflow");
+    for (const long long *stride : strides)
+        if (!reach_ok(rows, *stride)) return fail(WKV7_ERR_ARG, "sizes overflow");
     return WKV7_OK;
 }
 
-// Bytes that `rows` rows of `width` elements reach over, `stride` elements apart.
+// Bytes that `rows` rows of `width` elements reach over, `stride` elements apart (reach_ok).
 size_t strided_bytes(size_t rows, size_t width, long long stride, wkv7_dtype dt) {
     return rows ? ((rows - 1) * static_cast<size_t>(stride) + width) * elem_bytes(dt) : 0;
 }
@@ -1016,6 +1021,7 @@ wkv7_status wkv7_beam_select(int B, int K, int V, int M, wkv7_dtype dt, const vo
     if (dt != WKV7_F32 && dt != WKV7_BF16) return fail(WKV7_ERR_ARG, "unknown dtype %d", (int)dt);
     if (row_stride == 0) row_stride = V;
     if (row_stride < V || row_stride > (1ll << 40)) return fail(WKV7_ERR_ARG, "row_stride=%lld: at least V=%d", row_stride, V);
+    if (!reach_ok(size_t(B) * K, row_stride)) return fail(WKV7_ERR_ARG, "sizes overflow");
     if (finished && (eos < 0 || eos >= V)) return fail(WKV7_ERR_ARG, "eos=%d outside 0..%d", eos, V - 1);
     const size_t need = wkv7::beam_select_workspace(B, K, V, M), rows = size_t(B) * K, outs = size_t(B) * M * 4;
     if (!workspace || workspace_bytes < need)
