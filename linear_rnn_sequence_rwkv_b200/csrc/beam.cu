@@ -434,10 +434,10 @@ __global__ void __launch_bounds__(kT, NV > 4 ? 5 : 6) beam_part_kernel(const Bea
     }
 }
 
-// Order-preserving bits of a score; 0 for -inf and NaN, which are never chosen.
+// Order-preserving bits of a score; 0 for -inf and NaN, which are never chosen. -0 is 0.
 __device__ __forceinline__ unsigned long long score_bits(double x) {
     if (!(x > -INFINITY)) return 0ull;
-    const long long u = __double_as_longlong(x);
+    const long long u = __double_as_longlong(x + 0.);
     return u < 0 ? ~(unsigned long long)u : (unsigned long long)u | (kOne << 63);
 }
 __device__ __forceinline__ double score_value(unsigned long long o) {
