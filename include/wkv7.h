@@ -466,7 +466,8 @@ WKV7_API wkv7_status wkv7_delta_forward(int B, int T, int H, int Hk, int N, wkv7
  * dS_T [B][H][N][N] fp32 or NULL (zero). Outputs, dense and of dt: dq, dk [rows][Hk][N] (summed over
  * the value heads of a key head, in a fixed order), dv [rows][H][N], dg, dbeta [rows][H]; dS0
  * [B][H][N][N] fp32 or NULL, may equal dS_T (in place). Rows behind the last packed sequence are not
- * written. A log decay of -inf has gradient 0. Repeated calls give identical results.
+ * written. A log decay of -104 or less, whose exp is 0, has gradient 0, and so has the first of a sequence
+ * without S0. Repeated calls give identical results.
  * Workspace: wkv7_delta_backward_workspace_bytes(...) bytes, no initial contents, not shared by calls
  * that may overlap in time. Errors as wkv7_delta_forward, plus WKV7_ERR_WORKSPACE.
  */

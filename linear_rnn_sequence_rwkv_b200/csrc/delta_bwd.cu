@@ -297,14 +297,15 @@ __global__ void __launch_bounds__(RW * 32 + GROUPS * kGroup, (!F32 && NN == 64 &
 constexpr int GC = 64, GT = 512;        // tokens, threads (16 warps: 4 row blocks of 16 by 4 column groups)
 
 // Tokens t0 .. t0 + n - 1 of a sequence, number `slot` of all chunks; a key head, and `heads` of its value heads from
-// `first` on. n = 0: none left.
+// `first` on. n = 0: none left. opens: the sequence starts here.
 struct GradChunk {
     long long t0, slot;
-    int n, hk, first, heads, part;
+    int n, hk, first, heads, part, opens;
 };
 struct GradScalars {
     float ghi[GC], glo[GC], rk[GC], sq[GC], beta[GC], kin[GC], qin[GC], kout[GC], out[GC];
     float up[GC], down[GC];         // near: D_ij = up_i down_j
+    float open[GC];                 // 0 where nothing is left of the state before a token, 1 elsewhere
     float row[4][GC], tail[4][GC], col[4][GC], diag[GC], dq[4][GC], dk[4][GC];
     float ss[GT / 32];
     float whole;
@@ -465,9 +466,9 @@ __device__ __forceinline__ GradChunk grad_chunk(const DeltaArgs &p, unsigned &ta
         t0 += chunk * GC;
         if (chunk >= 0 && t0 < t1) {
             const int hk = whole - number * p.Hk, part = task - whole * parts, n = int(min((long long)GC, t1 - t0));
-            if (parts == 1) return {t0, slot, n, hk, hk * p.group, p.group, 0};
+            if (parts == 1) return {t0, slot, n, hk, hk * p.group, p.group, 0, chunk == 0};
             const int from = p.group * part / parts;
-            return {t0, slot, n, hk, hk * p.group + from, p.group * (part + 1) / parts - from, part};
+            return {t0, slot, n, hk, hk * p.group + from, p.group * (part + 1) / parts - from, part, chunk == 0};
         }
     }
     return {};
@@ -621,6 +622,7 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p, un
                             sc->ghi[i] = float(int(G[e] >> 22)) * 9.765625e-4f + bad;
                             sc->glo[i] = float(int(G[e] & 0x3fffff)) * 2.3283064365386963e-10f;
                             sc->beta[i] = b[e];
+                            sc->open[i] = g[e] <= -104.f || (i == 0 && cur->opens && !p.S0) ? 0.f : 1.f;    // exp(g) is 0
                             sc->kin[i] = in * sc->rk[i];
                             sc->qin[i] = in * sc->sq[i];
                             sc->kout[i] = to * sc->rk[i];
@@ -868,7 +870,9 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p, un
                 if (lane == 0) up = 0.f;
                 if (lane == 31) down = 0.f;
                 const float last = sc->whole * x;
-                const float dg[2] = {((dG[0] + dG[1]) + down) + (up + last), (dG[1] + down) + ((up + bt[0]) + last)};
+                // where nothing is left of the state before a token, the sums cancel but for their roundings (a NaN stays one)
+                const float dg[2] = {(((dG[0] + dG[1]) + down) + (up + last)) * sc->open[2 * lane],
+                                     ((dG[1] + down) + ((up + bt[0]) + last)) * sc->open[2 * lane + 1]};
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
                     if (2 * lane + e < n) {
