@@ -425,7 +425,10 @@ WKV7_API wkv7_status wkv7_decode_step_raw(int B, int H, int N, wkv7_dtype dt,
  * sequences of T tokens, or, with cu_seqlens, T packed rows of B sequences, sequence s holding the
  * rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1. States [B][H][N][N] fp32. H must be a multiple of Hk;
  * N is 64 or 128. g is a log decay: any value <= 0, -inf included (the state is reset); positive
- * values grow the state. beta is any finite value. In the forward and the step an input that is not finite
+ * values grow the state, by at most e^80 within each 32 tokens of a sequence (counted from its first): in the
+ * forward a token that exceeds this counts as one whose g is not finite. The backward takes 64 tokens at a
+ * time; where they grow the state by more than e^80 all gradients of the sequence and head may be lost (not
+ * finite). beta is any finite value. In the forward and the step an input that is not finite
  * reaches only its own and later tokens of its sequence: v its own value channel, k, g and beta all of
  * the heads they belong to, q its own token's outputs.
  * q, k and v may be strided by token (heads and channels dense): row strides in elements, multiples
