@@ -430,7 +430,8 @@ WKV7_API wkv7_status wkv7_decode_step_raw(int B, int H, int N, wkv7_dtype dt,
  * time; where they grow the state by more than e^80 all gradients of the sequence and head may be lost (not
  * finite). beta is any finite value. In the forward and the step an input that is not finite
  * reaches only its own and later tokens of its sequence: v its own value channel, k, g and beta all of
- * the heads they belong to, q its own token's outputs.
+ * the heads they belong to, q its own token's outputs. With qk_norm a q or k whose sum of squares is beyond
+ * fp32's range (a length of 1.8e19 and more) counts as one that is not finite.
  * q, k and v may be strided by token (heads and channels dense): row strides in elements, multiples
  * of 16 bytes, at least Hk * N (v: H * N).
  */

@@ -68,4 +68,8 @@ __device__ __forceinline__ void delta_rows(const int *cu, int T, int s, long lon
 // count as -120, so that differences of sums of decays stay finite; a NaN stays one.
 __device__ __forceinline__ float delta_clamp(float g) { return g < -120.f ? -120.f : g; }
 
+// What brings a vector of this sum of squares to unit length; NaN where the sum is not finite (it would be 0, and the
+// vector silently the zero vector, where finite elements have squares beyond fp32).
+__device__ __forceinline__ float delta_unit(float squares, float eps) { return rsqrtf(squares + eps) + 0.f * squares; }
+
 }  // namespace wkv7

@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(GT, 1) delta_grad_kernel(const DeltaArgs p, un
                             for (int e = 0; e < 8; ++e) l = fmaf(x[e], x[e], l);
                         }
                         l = quad_sum(l);
-                        l = p.qk_norm ? rsqrtf(l + p.norm_eps) : 1.f;
+                        l = p.qk_norm ? delta_unit(l, p.norm_eps) : 1.f;
                         if (part == 0) (tid < 256 ? sc->rk : sc->sq)[row] = tid < 256 ? l : l * p.scale;
                         __syncthreads();
                     }

@@ -347,7 +347,7 @@ __device__ __forceinline__ void prepare_chunk(uint32_t k, uint32_t q, unsigned c
         fine = len[0] + len[1] + len[2] + len[3] < INFINITY && fabsf(beta) < INFINITY;
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) len[r] = (p.qk_norm ? rsqrtf(len[r] + p.norm_eps) : 1.f) * (queries ? p.scale : 1.f);
+    for (int r = 0; r < 4; ++r) len[r] = (p.qk_norm ? delta_unit(len[r], p.norm_eps) : 1.f) * (queries ? p.scale : 1.f);
     if (tc == 0 && (TP > 0 || !queries)) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) (queries ? ps->rq : ps->rk)[gr + 8 * r] = len[r];

@@ -64,8 +64,8 @@ __global__ void __launch_bounds__(THREADS) delta_step_kernel(const DeltaArgs p) 
         for (int m = 0; m < RPT; ++m) vi[m] = load1(v + b * p.vs + rbase + RS * m);
         float rk = 1.f, rq = p.scale;
         if (p.qk_norm) {
-            rk = rsqrtf(lanes_sum(dot4(k4, k4)) + p.norm_eps);
-            rq *= rsqrtf(lanes_sum(dot4(q4, q4)) + p.norm_eps);
+            rk = delta_unit(lanes_sum(dot4(k4, k4)), p.norm_eps);
+            rq *= delta_unit(lanes_sum(dot4(q4, q4)), p.norm_eps);
         }
 #pragma unroll
         for (int m = 0; m < RPT; ++m) {

@@ -118,3 +118,35 @@ def test_gradients_of_states_that_grow(cuda_device, gates, N, dt):
     for n in ("dq", "dk", "dv", "dg", "dbeta"):
         assert slice_rel_err(got[n], ref[n], (0, 2)) <= (Y_TOL["bf16"] if dt == "bf16" else 4e-5), n
     assert slice_rel_err(got["dS0"], ref["dS0"], (0, 1)) <= 4e-5
+# ---- keys and queries whose squares leave fp32 -------------------------------------------------------
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [64, 128])
+@pytest.mark.parametrize("t", [0, 45, 69])
+def test_lengths_beyond_fp32_are_not_finite(cuda_device, t, N, dt):
+    """With qk_norm a key or query whose sum of squares overflows fp32 counts as one that is not finite."""
+    d = make((1, 70), 4, 2, N, dt, seed=75)
+    ref, S_ref = wkv7.delta_forward(*to(d, cuda_device).values(), qk_norm=True)
+    for name in "kq":
+        x = {n: v.clone() for n, v in d.items()}
+        x[name][0, t, 1, 5] = 1e20
+        y, S = wkv7.delta_forward(*to(x, cuda_device).values(), qk_norm=True)
+        assert torch.equal(y[:, :, :2], ref[:, :, :2]) and torch.equal(S[:, :2], S_ref[:, :2])
+        tol = Y_TOL[dt] * float(ref.abs().max())
+        assert t == 0 or float((y[:, :t, 2:] - ref[:, :t, 2:]).abs().max()) <= tol
+        if name == "k":
+            assert not bool(torch.isfinite(y[:, t:, 2:]).any()) and not bool(torch.isfinite(S[:, 2:]).any())
+        else:
+            assert not bool(torch.isfinite(y[:, t, 2:]).any()) and torch.equal(S, S_ref)
+            assert t == 69 or float((y[:, t + 1:, 2:] - ref[:, t + 1:, 2:]).abs().max()) <= tol
+        one = {n: v[:, t].contiguous().to(cuda_device) for n, v in x.items()}
+        pool = state(1, 4, N, 6).to(cuda_device)
+        before = pool.clone()
+        y1 = wkv7.delta_step(*one.values(), pool, qk_norm=True)
+        assert bool(torch.isfinite(y1[:, :2]).all()) and bool(torch.isfinite(pool[:, :2]).all())
+        assert not bool(torch.isfinite(y1[:, 2:]).any())
+        assert bool(torch.isfinite(pool[:, 2:]).any()) == (name == "q")
+        assert not torch.equal(pool[:, :2], before[:, :2])
+        dy = torch.ones_like(x["v"]).to(cuda_device)
+        g = wkv7.delta_backward(*to(x, cuda_device).values(), dy, qk_norm=True)
+        assert not bool(torch.isfinite(g["d" + name][0, t, 1]).any())
