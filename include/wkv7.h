@@ -431,7 +431,8 @@ WKV7_API wkv7_status wkv7_decode_step_raw(int B, int H, int N, wkv7_dtype dt,
  * finite). beta is any finite value. In the forward and the step an input that is not finite
  * reaches only its own and later tokens of its sequence: v its own value channel, k, g and beta all of
  * the heads they belong to, q its own token's outputs. With qk_norm a q or k whose sum of squares is beyond
- * fp32's range (a length of 1.8e19 and more) counts as one that is not finite.
+ * fp32's range (a length of 1.8e19 and more) counts as one that is not finite, and so may an fp32 input beyond
+ * bf16's largest number (3.39e38) in the forward.
  * q, k and v may be strided by token (heads and channels dense): row strides in elements, multiples
  * of 16 bytes, at least Hk * N (v: H * N).
  */

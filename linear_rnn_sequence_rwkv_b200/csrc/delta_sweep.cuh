@@ -36,13 +36,16 @@ struct Layout {
     static constexpr int threads = RW * 32 + GROUPS * kGroup, meet = RW * 32 + kGroup;
 };
 
-// Values that are not finite leave the products (0) and their places the mask: bit 4 n + e.
+// Below it a number's first bf16 term is finite; from it on, up to fp32's own largest, the terms would be infinite.
+constexpr float kTermMost = 0x1.ffp127f;
+
+// Values that are not finite (or as good as that: kTermMost) leave the products (0) and their places the mask: bit 4 n + e.
 __device__ __forceinline__ void take_out(float (&x)[4][4], uint32_t &mask) {
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const bool ok = fabsf(x[n][e]) < INFINITY;
+            const bool ok = fabsf(x[n][e]) < kTermMost;
             mask |= ok ? 0u : 1u << (4 * n + e);
             x[n][e] = ok ? x[n][e] : 0.f;
         }
@@ -238,7 +241,7 @@ __device__ __forceinline__ void forward_sweep(const DeltaArgs &p, unsigned block
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) z = fmaf(V[n][e], 0.f, z);
+                for (int e = 0; e < 4; ++e) z += fabsf(V[n][e]) < kTermMost ? 0.f : 1.f;
         }
         // A value that is not finite makes its row so from its token on and no earlier, which products with
         // the zeros of W and P would not keep. In a chunk with such inputs (NaN or infinite v, k, g or beta)

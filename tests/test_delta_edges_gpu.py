@@ -150,3 +150,22 @@ def test_lengths_beyond_fp32_are_not_finite(cuda_device, t, N, dt):
         dy = torch.ones_like(x["v"]).to(cuda_device)
         g = wkv7.delta_backward(*to(x, cuda_device).values(), dy, qk_norm=True)
         assert not bool(torch.isfinite(g["d" + name][0, t, 1]).any())
+# ---- fp32 beyond bf16's range -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("N", [64, 128])
+@pytest.mark.parametrize("t", [0, 45, 69])
+@pytest.mark.parametrize("value", [torch.finfo(torch.float32).min, 3.4e38])
+def test_values_beyond_the_range_of_bf16(cuda_device, value, t, N):
+    """Operands are split into bf16 terms, the largest of which is 3.39e38: an fp32 value above it counts as infinite,
+    and like one reaches its own channel from its token on and nothing else."""
+    d = make((1, 70), 2, 2, N, "f32", seed=76)
+    ref, S_ref = wkv7.delta_forward(*to(d, cuda_device).values(), qk_norm=True)
+    d["v"][0, t, 1, 7] = value
+    y, S = wkv7.delta_forward(*to(d, cuda_device).values(), qk_norm=True)
+    rest = [i for i in range(N) if i != 7]
+    tol = Y_TOL["f32"] * float(ref.abs().max())
+    assert torch.equal(y[:, :, 0], ref[:, :, 0])
+    assert float((y[..., rest] - ref[..., rest]).abs().max()) <= tol
+    assert t == 0 or float((y[:, :t] - ref[:, :t]).abs().max()) <= tol
+    assert not bool(torch.isfinite(y[0, t:, 1, 7]).any()) and not bool(torch.isfinite(S[0, 1, 7]).any())
+    assert bool(torch.isfinite(S[0, 1, rest]).all())
