@@ -510,8 +510,8 @@ WKV7_API wkv7_status wkv7_delta_step(int B, int H, int Hk, int N, wkv7_dtype dt,
  * (masked tokens, dead beams) is never chosen; a NaN logit counts as -inf, and a row with +inf has
  * no normalised scores and offers nothing. Where fewer than M continuations exist the
  * rest of the outputs hold score -inf, parent -1 and token -1.
- * logits   [B][K] rows of V elements of dt, row_stride elements apart (0 = V); any alignment of
- *          the elements (the base pointer 16-byte aligned as everywhere).
+ * logits   [B][K] rows of V elements of dt, row_stride elements apart (0 = V), aligned to their
+ *          elements only (the other pointers are 16-byte aligned as everywhere).
  * scores   [B][K] fp32.      finished [B][K] bytes (0 or 1) or NULL; eos in 0..V-1 when given.
  * Outputs  out_scores [B][M] fp32, parents [B][M] int32 (the beam j), tokens [B][M] int32.
  * Sizes: B, V >= 1, 1 <= K <= 64, 1 <= M <= 64. The normaliser is summed in fp32 per thread and

@@ -92,6 +92,7 @@ struct Buf {
     const char *name;
     const void *ptr;
     size_t bytes;
+    size_t align = 16;
 };
 
 // Device-side checks of one buffer: device memory of the current device, large enough.
@@ -672,7 +673,8 @@ template <class Allowed>
 wkv7_status check_buffers(const Buf *bufs, int n, int first_out, Allowed allowed) {
     for (int i = 0; i < n; ++i) {
         if (bufs[i].bytes && !bufs[i].ptr) return fail(WKV7_ERR_ARG, "%s is NULL", bufs[i].name);
-        if (bufs[i].ptr && !aligned16(bufs[i].ptr)) return fail(WKV7_ERR_ALIGN, "%s is not 16-byte aligned", bufs[i].name);
+        if (reinterpret_cast<uintptr_t>(bufs[i].ptr) % bufs[i].align)
+            return fail(WKV7_ERR_ALIGN, "%s is not %zu-byte aligned", bufs[i].name, bufs[i].align);
     }
     for (int o = first_out; o < n; ++o)
         for (int i = 0; i < n; ++i)
@@ -1026,7 +1028,7 @@ wkv7_status wkv7_beam_select(int B, int K, int V, int M, wkv7_dtype dt, const vo
     const size_t need = wkv7::beam_select_workspace(B, K, V, M), rows = size_t(B) * K, outs = size_t(B) * M * 4;
     if (!workspace || workspace_bytes < need)
         return fail(WKV7_ERR_WORKSPACE, "workspace of %zu bytes required, %zu given", need, workspace ? workspace_bytes : 0);
-    const Buf bufs[] = {{"logits", logits, strided_bytes(rows, V, row_stride, dt)},
+    const Buf bufs[] = {{"logits", logits, strided_bytes(rows, V, row_stride, dt), elem_bytes(dt)},
                         {"scores", scores, rows * 4},
                         {"finished", finished, finished ? rows : 0},
                         {"out_scores", out_scores, outs},

@@ -51,14 +51,15 @@ __device__ __forceinline__ unsigned long long make_key(float x, uint32_t index) 
 
 // A thread's vectors from a row that starts SHIFT elements behind a 16-byte boundary: each is two aligned ones, shifted
 // together. Rows of an odd vocabulary start anywhere; equal rows must be cut into the same vectors all the same, so that
-// their sums, and with them ties between beams, come out equal. Vectors from behind `most` are left out.
+// their sums, and with them ties between beams, come out equal. Vectors from behind `most` are left out, and so is the
+// first where it `opens` a buffer that starts anywhere.
 template <class Tin, int NV, int STEP, int SHIFT>
-__device__ __forceinline__ void load_shifted(uint4 (&v)[NV], const Tin *row, int at, int most) {
+__device__ __forceinline__ void load_shifted(uint4 (&v)[NV], const Tin *row, int at, int most, bool opens) {
     constexpr int q = SHIFT * int(sizeof(Tin)) / 4, half = SHIFT * int(sizeof(Tin)) % 4;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int i = at + j * STEP;
-        if (i > most) continue;
+        if (i > most || (j == 0 && opens)) continue;
         const uint4 *a = reinterpret_cast<const uint4 *>(row + i - SHIFT);
         if constexpr (SHIFT == 0) {
             v[j] = __ldg(a);
@@ -73,25 +74,25 @@ __device__ __forceinline__ void load_shifted(uint4 (&v)[NV], const Tin *row, int
     }
 }
 template <int NV, int STEP>
-__device__ __forceinline__ void load_row(uint4 (&v)[NV], const float *row, int shift, int at, int most) {
+__device__ __forceinline__ void load_row(uint4 (&v)[NV], const float *row, int shift, int at, int most, bool opens) {
     switch (shift) {
-        case 0: return load_shifted<float, NV, STEP, 0>(v, row, at, most);
-        case 1: return load_shifted<float, NV, STEP, 1>(v, row, at, most);
-        case 2: return load_shifted<float, NV, STEP, 2>(v, row, at, most);
-        default: return load_shifted<float, NV, STEP, 3>(v, row, at, most);
+        case 0: return load_shifted<float, NV, STEP, 0>(v, row, at, most, opens);
+        case 1: return load_shifted<float, NV, STEP, 1>(v, row, at, most, opens);
+        case 2: return load_shifted<float, NV, STEP, 2>(v, row, at, most, opens);
+        default: return load_shifted<float, NV, STEP, 3>(v, row, at, most, opens);
     }
 }
 template <int NV, int STEP>
-__device__ __forceinline__ void load_row(uint4 (&v)[NV], const __nv_bfloat16 *row, int shift, int at, int most) {
+__device__ __forceinline__ void load_row(uint4 (&v)[NV], const __nv_bfloat16 *row, int shift, int at, int most, bool opens) {
     switch (shift) {
-        case 0: return load_shifted<__nv_bfloat16, NV, STEP, 0>(v, row, at, most);
-        case 1: return load_shifted<__nv_bfloat16, NV, STEP, 1>(v, row, at, most);
-        case 2: return load_shifted<__nv_bfloat16, NV, STEP, 2>(v, row, at, most);
-        case 3: return load_shifted<__nv_bfloat16, NV, STEP, 3>(v, row, at, most);
-        case 4: return load_shifted<__nv_bfloat16, NV, STEP, 4>(v, row, at, most);
-        case 5: return load_shifted<__nv_bfloat16, NV, STEP, 5>(v, row, at, most);
-        case 6: return load_shifted<__nv_bfloat16, NV, STEP, 6>(v, row, at, most);
-        default: return load_shifted<__nv_bfloat16, NV, STEP, 7>(v, row, at, most);
+        case 0: return load_shifted<__nv_bfloat16, NV, STEP, 0>(v, row, at, most, opens);
+        case 1: return load_shifted<__nv_bfloat16, NV, STEP, 1>(v, row, at, most, opens);
+        case 2: return load_shifted<__nv_bfloat16, NV, STEP, 2>(v, row, at, most, opens);
+        case 3: return load_shifted<__nv_bfloat16, NV, STEP, 3>(v, row, at, most, opens);
+        case 4: return load_shifted<__nv_bfloat16, NV, STEP, 4>(v, row, at, most, opens);
+        case 5: return load_shifted<__nv_bfloat16, NV, STEP, 5>(v, row, at, most, opens);
+        case 6: return load_shifted<__nv_bfloat16, NV, STEP, 6>(v, row, at, most, opens);
+        default: return load_shifted<__nv_bfloat16, NV, STEP, 7>(v, row, at, most, opens);
     }
 }
 __device__ __forceinline__ void unpack(const uint4 v, float (&x)[4]) {
@@ -260,7 +261,9 @@ __global__ void __launch_bounds__(kT, NV > 4 ? 5 : 6) beam_part_kernel(const Bea
     const int most = p.V - VW - (shift ? VW - shift : 0);  // last place from which a whole (shifted) vector may be read
     const int at = split * SEG + tid * VW;                 // V + 65536 fits an int
     uint4 v[NV] = {};
-    load_row<NV, kT * VW>(v, base, shift, at, most);
+    const bool opens = shift != 0 && row == 0 && at == 0;
+    load_row<NV, kT * VW>(v, base, shift, at, most, opens);
+    if (opens) v[0] = load_edge(base, 0, p.V);
     if (at + (NV - 1) * kT * VW > most) {                  // the row ends here
 #pragma unroll
         for (int j = 0; j < NV; ++j)

@@ -43,3 +43,18 @@ def test_logits_stride(lib):
     assert lib.wkv7_beam_select((1 << 23) + 1, 1, 100, 2, wkv7.BF16, p[0], WIDE, p[1], p[2], 0, *p[3:], 1 << 40,
                                 None) == wkv7.ERR_ARG
     assert b"overflow" in lib.wkv7_last_error()
+
+
+@pytest.mark.parametrize("dt,off", [(wkv7.F32, 1), (wkv7.F32, 2), (wkv7.BF16, 1), (wkv7.BF16, 3)])
+def test_logits_are_aligned_to_their_elements(lib, dt, off):
+    p = _ptrs(7)
+    assert lib.wkv7_beam_select(1, 2, 100, 2, dt, ctypes.c_void_p(BASE + off), 0, p[1], p[2], 0, *p[3:], 1 << 20, None) == wkv7.ERR_ALIGN
+    assert b"logits" in lib.wkv7_last_error()
+
+
+@pytest.mark.parametrize("dt,off", [(wkv7.F32, 4), (wkv7.BF16, 2)])
+def test_logits_that_start_anywhere_may_not_overlap_outputs(lib, dt, off):
+    p = _ptrs(7)
+    at = ctypes.c_void_p(p[3].value - off)
+    assert lib.wkv7_beam_select(1, 2, 100, 2, dt, at, 0, p[1], p[2], 0, *p[3:], 1 << 20, None) == wkv7.ERR_ARG
+    assert b"overlaps" in lib.wkv7_last_error()
