@@ -505,7 +505,9 @@ WKV7_API wkv7_status wkv7_delta_step(int B, int H, int Hk, int N, wkv7_dtype dt,
  * One step of beam search's selection: of the K beams of each of B requests and the V tokens of the
  * vocabulary, the M best continuations by
  *     score(b, j, t) = scores[b][j] + logits[b][j][t] - log(sum_t' exp(logits[b][j][t']))
- * from the best down; equal scores go to the lowest j * V + t. A beam marked in `finished` offers
+ * from the best down; equal scores go to the lowest j * V + t. The tokens of one beam are compared by their
+ * logits, also where its score is so large (as the lowest value that marks a dead beam) that the sum no longer tells
+ * them apart; equal sums of two beams go to the lower beam. A beam marked in `finished` offers
  * only the token eos, at its own score (nothing is read of its logits). A score of -inf or NaN
  * (masked tokens, dead beams) is never chosen; a NaN logit counts as -inf, and a row with +inf has
  * no normalised scores and offers nothing. Where fewer than M continuations exist the

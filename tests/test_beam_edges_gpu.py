@@ -56,3 +56,18 @@ def test_logits_of_the_last_position(cuda_device, dt):
     got = wkv7.beam_select(xd[:, :, -1], s.to(cuda_device), M)
     want = delta.beam_select(x[:, :, -1].double().numpy(), s.numpy(), M)
     assert np.array_equal(got[1].cpu().numpy(), want[1]) and np.array_equal(got[2].cpu().numpy(), want[2])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_beams_at_the_lowest_score_offer_their_tokens_by_logit(cuda_device, dt):
+    """The tokens of one beam come in the order of their logits, whatever its score leaves of their differences."""
+    g = torch.Generator().manual_seed(6)
+    x = (3 * torch.randn(1, 3, 501, generator=g)).to(DT[dt])
+    low = torch.finfo(torch.float32).min
+    got = wkv7.beam_select(x.to(cuda_device), torch.full((1, 3), low, device=cuda_device), 7)
+    order = torch.sort(x[0, 0].float(), descending=True, stable=True).indices[:7]
+    assert got[1].tolist() == [[0] * 7] and got[2].cpu().tolist() == [order.tolist()]
+    assert bool(torch.all(got[0] == low))
+    s = torch.tensor([[low, -3.0, low]])
+    got = wkv7.beam_select(x.to(cuda_device), s.to(cuda_device), 7)
+    assert got[1].tolist() == [[1] * 7]
