@@ -683,6 +683,15 @@ def _plain(name, t, shape, dtype, dev):
         _wrong(name, t, shape, dtype, dev)
 
 
+def _workspace(t, need, dev):
+    """The caller's workspace where it is large enough, else a new one (None if none is needed), and its bytes."""
+    if t is not None and not t.is_contiguous():     # what lies between its elements would be overwritten
+        raise ValueError("workspace must be contiguous")
+    if need and (t is None or t.numel() * t.element_size() < need):
+        t = torch.empty(need, device=dev, dtype=torch.uint8)
+    return t, 0 if t is None else t.numel() * t.element_size()
+
+
 def _row_stride(name, t, shape, dtype, dev):
     """Elements from one token's row to the next of a tensor whose heads and channels are dense and
     whose rows are evenly spaced over all leading dimensions (0 for the dense layout, or a single row).
@@ -806,9 +815,7 @@ def delta_backward(q, k, v, g, beta, dy, S0=None, dS_T=None, *, scale=None, qk_n
         elif return_state_grad:
             dS0 = torch.empty(states, device=dev, dtype=torch.float32)
         need = lib.wkv7_delta_backward_workspace_bytes(B, T, H, Hk, N, dt, o)
-        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-            workspace = torch.empty(need, device=dev, dtype=torch.uint8)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        workspace, ws_bytes = _workspace(workspace, need, dev)
         st = lib.wkv7_delta_backward(B, T, H, Hk, N, dt, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
                                      beta.data_ptr(), _at(S0), dy.data_ptr(), _at(dS_T),
                                      *(grads[n].data_ptr() for n in DELTA_GRAD_NAMES), _at(dS0), o, _at(workspace),
@@ -869,9 +876,7 @@ def beam_select(logits, scores, M, *, finished=None, eos=0, out=None, workspace=
             for n, t, d in zip(("scores", "parents", "tokens"), out, (torch.float32, torch.int32, torch.int32)):
                 _plain("out " + n, t, (B, M), d, dev)
         need = lib.wkv7_beam_select_workspace_bytes(B, K, V, M)
-        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-            workspace = torch.empty(need, device=dev, dtype=torch.uint8)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        workspace, ws_bytes = _workspace(workspace, need, dev)
         st = lib.wkv7_beam_select(B, K, V, M, dt, logits.data_ptr(), stride, scores.data_ptr(), _at(finished), eos,
                                   out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), _at(workspace), ws_bytes,
                                   handle)

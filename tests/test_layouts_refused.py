@@ -71,3 +71,16 @@ def test_a_scale_of_zero(scale):
         wkv7.delta_backward(*d.values(), torch.zeros_like(d["v"]), scale=scale)
     with pytest.raises(ValueError, match="scale"):
         wkv7.delta_step(*(x[0] for x in d.values()), torch.zeros(3, 4, 64, 64), scale=scale)
+
+
+def test_a_workspace_with_gaps():
+    """Its elements' bytes would count as dense, and what lies between them be overwritten."""
+    cpu = torch.device("cpu")
+    with pytest.raises(ValueError, match="workspace"):
+        wkv7._workspace(torch.zeros(100, dtype=torch.uint8)[::2], 40, cpu)
+    with pytest.raises(ValueError, match="workspace"):
+        wkv7._workspace(torch.zeros(1).expand(100), 40, cpu)
+    own = torch.zeros(20)
+    assert wkv7._workspace(own, 80, cpu)[0] is own and wkv7._workspace(own, 80, cpu)[1] == 80
+    new, size = wkv7._workspace(own, 81, cpu)
+    assert new is not own and size == 81 and wkv7._workspace(None, 0, cpu) == (None, 0)
