@@ -44,7 +44,7 @@ struct DeltaArgs {
 
 cudaError_t launch_delta_forward(const DeltaArgs &p);
 cudaError_t launch_delta_step(const DeltaArgs &p);
-cudaError_t launch_delta_backward(const DeltaArgs &p);      // both kernels of the backward
+cudaError_t launch_delta_backward(const DeltaArgs &p);      // two to four launches: the sweeps, the gradients, their sum
 size_t delta_backward_workspace(size_t rows, int B, int H, int Hk, int N, wkv7_dtype dt);
 
 // Chunks of 64 tokens are numbered over all sequences so that each has a place of its own without a pass over

@@ -1,4 +1,5 @@
-// The gated delta rule's backward, in two kernels. With the chunk quantities of delta_sweep.cuh and
+// The gated delta rule's backward: two sweeps, in one launch or two, then the gradients, and where a key head's value
+// heads are divided the sum of the parts. With the chunk quantities of delta_sweep.cuh and
 // dS' the gradient of a chunk's last state:
 //   1. the forward sweep (delta_sweep.cuh, STATES): the errors E, and the state every 64 tokens start from;
 //   2. the reverse sweep: the chain back through the chunks of 32,

@@ -181,8 +181,6 @@ struct Scalars {
     float kin[C];    // exp(G_i) / |k_i|: applied to S k_i
     float qin[C];    // scale exp(G_i) / |q_i|: applied to S q_i
     float out[C];    // exp(G_C - G_j) beta_j / |k_j|: applied to e_j in the state's update
-    float kout[C];   // exp(G_C - G_j) / |k_j| (backward)
-    float beta[C];
     float whole;     // exp(G_C)
     int odd;         // a key or gate of the chunk is not finite, or the state may grow beyond fp32
     float pad[2];
@@ -383,9 +381,7 @@ __device__ __forceinline__ void prepare_chunk(uint32_t k, uint32_t q, unsigned c
         const float out = (nan ? bad : expf(float(rest) * 2.3283064365386963e-10f)) * rk;
         sc->kin[lane] = in * rk;
         if constexpr (TP > 0) sc->qin[lane] = in * ps->rq[lane];
-        sc->kout[lane] = out;
         sc->out[lane] = out * beta;
-        sc->beta[lane] = beta;
         if (lane == 31) sc->whole = nan ? bad : in;
         if constexpr (TP == 0) return;
     }

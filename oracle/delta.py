@@ -82,17 +82,6 @@ def delta_backward(q, k, v, g, beta, S0, dy, dS_T, *, scale=None, qk_norm=False,
     return out
 
 
-def packed(fn, cu, tensors, states, **kw):
-    """``fn`` (one of the above) on each sequence of packed rows: ``tensors`` [rows, ...] cut at
-    ``cu``, ``states`` [B, ...] one each (or None). Returns the results' lists, one per sequence."""
-    out = []
-    for s, (a, b) in enumerate(zip(cu[:-1], cu[1:])):
-        cut = [x[a:b][None] for x in tensors]
-        st = [None if x is None else x[s:s + 1] for x in states]
-        out.append(fn(cut, st, **kw))
-    return out
-
-
 def beam_select(logits, scores, M, finished=None, eos=0):
     """Every continuation scored, sorted from the best down (equal scores: lowest beam, then lowest
     token); fewer than M: score -inf, parent and token -1."""
