@@ -517,7 +517,9 @@ WKV7_API wkv7_status wkv7_delta_step(int B, int H, int Hk, int N, wkv7_dtype dt,
  * scores   [B][K] fp32.      finished [B][K] bytes (0 or 1) or NULL; eos in 0..V-1 when given.
  * Outputs  out_scores [B][M] fp32, parents [B][M] int32 (the beam j), tokens [B][M] int32.
  * Sizes: B, V >= 1, 1 <= K <= 64, 1 <= M <= 64. The normaliser is summed in fp32 per thread and
- * in fp64 across threads, and scores are compared in fp64 before they are rounded to fp32.
+ * in fp64 across threads, and scores are compared in fp64 before they are rounded to fp32. The normaliser's
+ * own rounding, about 1e-7, decides between two beams whose scores are closer than that; beams with equal logits
+ * get equal normalisers.
  * Workspace: wkv7_beam_select_workspace_bytes(B, K, V, M) bytes.
  * Errors as wkv7_delta_forward, plus WKV7_ERR_WORKSPACE; WKV7_ERR_UNSUPPORTED for K or M above 64.
  */

@@ -11,7 +11,7 @@
 // complement of the index, so that keys never tie and equal values go to the lowest index.
 // beam_pick_kernel: one CTA per request joins the segments' sums in fp64, merges the sorted lists of a row and
 // then those of the rows.
-// 64 requests of 8 beams over 50277 bf16 logits (51.5 MB): 29 us, of which the segments 24 (2.1 TB/s; issue 62 %, 715
+// 64 requests of 8 beams over 50277 bf16 logits (51.5 MB): 28 us, of which the segments 24 (2.1 TB/s; issue 62 %, 715
 // instructions per warp of 1280 logits, 140 of them for the exponentials); 27 us where rows are aligned to 16 bytes.
 // One request of 4 beams over 65536 fp32 logits: 8.4 us.
 #include "beam.cuh"
